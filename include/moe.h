@@ -274,6 +274,175 @@ int moe_quantize_1x128(const void* x, int64_t rows, int32_t cols, uint8_t* q, fl
                        void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The operators around the expert layer: what the rest of a decoder block's
+ * feed-forward half needs.  Norms with the residual stream between two blocks,
+ * the dense gated feed-forward block of the layers that have no experts (or of
+ * the shared expert on its own), and projections into and out of the stream.
+ *
+ * The conventions above hold.  Further, for all of them:
+ *  - dtype is the one type of every tensor of a call, MOE_F32 or MOE_BF16 (else
+ *    MOE_ERR_DTYPE): activations, parameters and their gradients.  Everything
+ *    between is float32 or, for the operands of a later product, rounded once
+ *    to bfloat16 (F32: not rounded; products of float32 operands keep float32's
+ *    precision).  Parameter gradients have their parameter's type: those of
+ *    products are made of bfloat16 operands, whose rounding a wider store
+ *    would only preserve.
+ *  - Activations are rows of contiguous elements, `ld_*` elements apart: any
+ *    ld >= the row's length and < 2^22 (else MOE_ERR_SHAPE), so columns of a
+ *    wider tensor can be passed; pointers are aligned to their element.
+ *    Parameters and their gradients are packed.  Rows, sizes and strides need
+ *    no alignment; multiples of 8 elements on 16-byte aligned pointers are
+ *    fastest (no operand is then laid out anew).
+ *  - T <= 2^24 and sizes <= 131072, else MOE_ERR_SHAPE.
+ *  - Workspaces are aligned to 16 bytes (else MOE_ERR_WORKSPACE).  Outputs may
+ *    not overlap inputs or each other, but where stated.
+ *  - T == 0 returns MOE_OK and writes nothing, gradients included.
+ *  - moe_profile_* does not record them.
+ */
+
+enum moe_act { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 /* z Phi(z) */ };
+
+enum moe_norm_kind { MOE_NORM_RMS = 0, MOE_NORM_LAYER = 1 };
+
+/*
+ * Norms after one block and before the next, with the gate and the residual
+ * scale between them.  Per token, for the residual stream r and the block's
+ * output f:
+ *   n = unit(f) * w_post + b_post       (no w_post: n = f)
+ *   u = res_scale * r + gate * n        (no gate: 1; no f: u = res_scale * r)
+ *   h = unit(u) * w_pre + b_pre
+ *   unit(v) = (v - m) / sqrt(mean((v - m)^2) + eps), m = mean(v) (LAYER) or 0 (RMS)
+ * u is the new residual stream, h the next block's input.
+ *   hidden     1 .. 16384, else MOE_ERR_SHAPE
+ *   gate_rows  consecutive tokens that share a row of gate: gate is
+ *              [T / gate_rows][hidden], so T (one row for the call: a layer
+ *              scale), a sequence's length (a row for each sequence) or 1.
+ *              0: no gate.  T % gate_rows != 0: MOE_ERR_SHAPE
+ *   eps        finite and >= 0, res_scale finite, else MOE_ERR_SHAPE
+ */
+typedef struct moe_norm_cfg {
+  int32_t hidden;
+  int32_t dtype;     /* moe_dtype */
+  int32_t kind;      /* moe_norm_kind, else MOE_ERR_SHAPE */
+  int32_t gate_rows;
+  float eps;
+  float res_scale;
+} moe_norm_cfg;
+
+/* Device pointers to [hidden] each (gate as above); NULL = absent.  Biases
+ * belong to MOE_NORM_LAYER (MOE_ERR_SHAPE with RMS), b_post needs w_post; gate
+ * is required if and only if gate_rows > 0 (else MOE_ERR_NULL / MOE_ERR_SHAPE).
+ * w_post, b_post and the gate need a branch (else MOE_ERR_NULL). */
+typedef struct moe_norm_params {
+  const void* w_post;
+  const void* b_post;
+  const void* w_pre;
+  const void* b_pre;
+  const void* gate;
+} moe_norm_params;
+
+/*
+ *   residual  device [T][hidden];  branch: the same, or NULL
+ *   u         out, or NULL; may be residual itself (same ld)
+ *   h         out, or NULL (then w_pre is not read); one of u and h is required
+ * h is formed from the unrounded u.  u and h may be branch itself (same ld).
+ */
+int moe_norm_forward(const moe_norm_cfg* cfg, int64_t T, const void* residual, int64_t ld_residual,
+                     const void* branch, int64_t ld_branch, const moe_norm_params* params, void* u,
+                     int64_t ld_u, void* h, int64_t ld_h, void* stream);
+
+/* Gradient outputs (device); NULL = not wanted.  Those of the activations are
+ * [T][hidden], the others shaped as their parameters. */
+typedef struct moe_norm_grads {
+  void* d_residual;
+  int64_t ld_d_residual;
+  void* d_branch;
+  int64_t ld_d_branch;
+  void* dw_post;
+  void* db_post;
+  void* dw_pre;
+  void* db_pre;
+  void* dgate;
+} moe_norm_grads;
+
+/*
+ * Gradients of <du, u> + <dh, h>; u and h are recomputed from residual and
+ * branch.  du or dh may be NULL (zero), not both.  A gradient whose parameter
+ * or branch is absent must be NULL, dw_pre and db_pre also without dh (else
+ * MOE_ERR_NULL).  d_residual may be du, and d_branch may be dh or branch
+ * (same ld).  Sums over tokens run in a fixed order, in float32.
+ */
+size_t moe_norm_backward_workspace_bytes(const moe_norm_cfg* cfg, int64_t T);
+int moe_norm_backward(const moe_norm_cfg* cfg, int64_t T, const void* residual, int64_t ld_residual,
+                      const void* branch, int64_t ld_branch, const moe_norm_params* params,
+                      const void* du, int64_t ld_du, const void* dh, int64_t ld_dh,
+                      const moe_norm_grads* grads, void* ws, size_t ws_bytes, void* stream);
+
+/* A projection: in_dim -> out_dim (1 .. 131072 each, else MOE_ERR_SHAPE), any moe_act. */
+typedef struct moe_linear_cfg {
+  int32_t in_dim;
+  int32_t out_dim;
+  int32_t act;    /* moe_act, else MOE_ERR_SHAPE */
+  int32_t dtype;  /* moe_dtype */
+} moe_linear_cfg;
+
+/*
+ * y = residual + act(x W^T + bias), in one pass over the products' sums.
+ *   x         device [T][in_dim];  w: [out_dim][in_dim]
+ *   bias      [out_dim] or NULL;   residual: [T][out_dim] or NULL
+ *   y         out [T][out_dim]; may be residual itself (same ld)
+ */
+size_t moe_linear_workspace_bytes(const moe_linear_cfg* cfg, int64_t T);
+int moe_linear_forward(const moe_linear_cfg* cfg, int64_t T, const void* x, int64_t ld_x,
+                       const void* w, const void* bias, const void* residual, int64_t ld_residual,
+                       void* y, int64_t ld_y, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradients of <dy, y> (the residual's is dy itself).  dx [T][in_dim],
+ * dw [out_dim][in_dim], dbias [out_dim]; each may be NULL (not wanted).  With
+ * an activation the sums before it are recomputed from x, w and bias.
+ */
+size_t moe_linear_backward_workspace_bytes(const moe_linear_cfg* cfg, int64_t T);
+int moe_linear_backward(const moe_linear_cfg* cfg, int64_t T, const void* x, int64_t ld_x,
+                        const void* w, const void* bias, const void* dy, int64_t ld_dy, void* dx,
+                        int64_t ld_dx, void* dw, void* dbias, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* A dense gated feed-forward block hidden -> inter -> hidden (1 .. 131072
+ * each); act: RELU, SILU or GELU, else MOE_ERR_SHAPE. */
+typedef struct moe_ffn_cfg {
+  int32_t hidden;
+  int32_t inter;
+  int32_t act;    /* moe_act */
+  int32_t dtype;  /* moe_dtype */
+} moe_ffn_cfg;
+
+/*
+ * y = residual + (act(x Wg^T) * (x Wu^T)) Wd^T: both projections, the
+ * activation and the product in one kernel, the product rounded to the operand
+ * type, then the down projection with the residual in its epilogue.
+ *   w_gate, w_up [inter][hidden], w_down [hidden][inter]: one expert's layout,
+ *                so the shared expert's matrices can be passed
+ *   residual     [T][hidden] or NULL;  y: out, may be residual itself (same ld)
+ */
+size_t moe_ffn_workspace_bytes(const moe_ffn_cfg* cfg, int64_t T);
+int moe_ffn_forward(const moe_ffn_cfg* cfg, int64_t T, const void* x, int64_t ld_x,
+                    const void* w_gate, const void* w_up, const void* w_down, const void* residual,
+                    int64_t ld_residual, void* y, int64_t ld_y, void* ws, size_t ws_bytes,
+                    void* stream);
+
+/*
+ * Gradients of <dy, y>: dx [T][hidden] and the weights' (the residual's is dy
+ * itself).  All are written; both projections are recomputed from x.
+ */
+size_t moe_ffn_backward_workspace_bytes(const moe_ffn_cfg* cfg, int64_t T);
+int moe_ffn_backward(const moe_ffn_cfg* cfg, int64_t T, const void* x, int64_t ld_x,
+                     const void* w_gate, const void* w_up, const void* w_down, const void* dy,
+                     int64_t ld_dy, void* dx, int64_t ld_dx, void* dw_gate, void* dw_up,
+                     void* dw_down, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Kernel timing instrumentation (off by default).  The state is per host
  * thread: moe_profile_enable switches it for the calling thread, whose
  * compute calls then record, and moe_profile_read reads that thread's record.

@@ -6,7 +6,9 @@ fallback: if the library is missing or the GPU is not a gfx950 device, calls
 raise.
 
 Entry points mirror the C ABI in ``include/moe.h``: :func:`workspace_bytes`,
-:func:`route`, :func:`forward`, :func:`bias_update`.
+:func:`route`, :func:`forward`, :func:`bias_update`; and, around the expert
+layer, :func:`norm_forward` / :func:`norm_backward`, :func:`linear_forward` /
+:func:`linear_backward` and :func:`ffn_forward` / :func:`ffn_backward`.
 """
 from __future__ import annotations
 
@@ -21,7 +23,14 @@ __all__ = ["F32", "BF16", "E4M3", "MoeError", "lib", "lib_path", "make_cfg", "cf
            "forward_noalloc", "NOALLOC_SCRATCH_BYTES",
            "bias_update", "quantize_1x128", "balance_loss", "backward", "backward_workspace_bytes",
            "alloc_backward_workspace", "profile_enable", "profile_read",
-           "status_string", "abi_version", "EXPORTED_SYMBOLS"]
+           "status_string", "abi_version", "EXPORTED_SYMBOLS",
+           "make_norm_cfg", "norm_forward", "norm_backward", "norm_backward_workspace_bytes",
+           "alloc_norm_backward_workspace",
+           "make_linear_cfg", "linear_forward", "linear_backward", "linear_workspace_bytes",
+           "linear_backward_workspace_bytes", "alloc_linear_workspace",
+           "alloc_linear_backward_workspace",
+           "make_ffn_cfg", "ffn_forward", "ffn_backward", "ffn_workspace_bytes",
+           "ffn_backward_workspace_bytes", "alloc_ffn_workspace", "alloc_ffn_backward_workspace"]
 
 F32, BF16, E4M3 = 0, 1, 2
 _DT_NAME = {"f32": F32, "bf16": BF16, "e4m3": E4M3}
@@ -31,7 +40,11 @@ EXPORTED_SYMBOLS = ("moe_workspace_bytes", "moe_route", "moe_forward", "moe_bias
                     "moe_profile_enable", "moe_profile_read", "moe_profile_kernel_name",
                     "moe_status_string", "moe_abi_version", "moe_quantize_1x128",
                     "moe_balance_loss", "moe_backward", "moe_backward_workspace_bytes",
-                    "moe_forward_noalloc")
+                    "moe_forward_noalloc",
+                    "moe_norm_forward", "moe_norm_backward", "moe_norm_backward_workspace_bytes",
+                    "moe_linear_forward", "moe_linear_backward", "moe_linear_workspace_bytes",
+                    "moe_linear_backward_workspace_bytes", "moe_ffn_forward", "moe_ffn_backward",
+                    "moe_ffn_workspace_bytes", "moe_ffn_backward_workspace_bytes")
 NOALLOC_SCRATCH_BYTES = 64 << 20    # MOE_NOALLOC_SCRATCH_BYTES of include/moe.h
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -61,6 +74,34 @@ class _Routing(ctypes.Structure):
 class _Experts(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("w_gate", "w_up", "w_down", "s_gate", "s_up",
                                                "s_down")]
+
+
+_ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}       # enum moe_act
+_NORM_KIND = {"rms": 0, "layer": 1}                        # enum moe_norm_kind
+
+
+class _NormCfg(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("gate_rows", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("res_scale", ctypes.c_float)]
+
+
+class _NormParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w_post", "b_post", "w_pre", "b_pre", "gate")]
+
+
+class _NormGrads(ctypes.Structure):
+    _fields_ = [("d_residual", ctypes.c_void_p), ("ld_d_residual", ctypes.c_int64),
+                ("d_branch", ctypes.c_void_p), ("ld_d_branch", ctypes.c_int64)] + \
+               [(n, ctypes.c_void_p) for n in ("dw_post", "db_post", "dw_pre", "db_pre", "dgate")]
+
+
+class _LinearCfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("in_dim", "out_dim", "act", "dtype")]
+
+
+class _FfnCfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("hidden", "inter", "act", "dtype")]
 
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -110,6 +151,22 @@ def lib() -> ctypes.CDLL:
         L.moe_quantize_1x128.restype = I32
         L.moe_profile_kernel_name.argtypes = [I32]
         L.moe_profile_kernel_name.restype = ctypes.c_char_p
+        C, V = ctypes.POINTER, I64
+        for name, args in (
+                ("norm_forward", [C(_NormCfg), I64, P, V, P, V, C(_NormParams), P, V, P, V, P]),
+                ("norm_backward", [C(_NormCfg), I64, P, V, P, V, C(_NormParams), P, V, P, V,
+                                   C(_NormGrads), P, SZ, P]),
+                ("linear_forward", [C(_LinearCfg), I64, P, V, P, P, P, V, P, V, P, SZ, P]),
+                ("linear_backward", [C(_LinearCfg), I64, P, V, P, P, P, V, P, V, P, P, P, SZ, P]),
+                ("ffn_forward", [C(_FfnCfg), I64, P, V, P, P, P, P, V, P, V, P, SZ, P]),
+                ("ffn_backward", [C(_FfnCfg), I64, P, V, P, P, P, P, V, P, V, P, P, P, P, SZ, P])):
+            fn = getattr(L, "moe_" + name)
+            fn.argtypes, fn.restype = args, I32
+        for name, cfg in (("norm_backward", _NormCfg), ("linear", _LinearCfg),
+                          ("linear_backward", _LinearCfg), ("ffn", _FfnCfg),
+                          ("ffn_backward", _FfnCfg)):
+            fn = getattr(L, f"moe_{name}_workspace_bytes")
+            fn.argtypes, fn.restype = [C(cfg), I64], SZ
         _LIB = L
     return _LIB
 
@@ -371,3 +428,207 @@ def bias_update(cfg: _Cfg, T: int, counts: torch.Tensor, bias: torch.Tensor, gam
                                ctypes.c_float(gamma), _stream(stream))
     if rc != 0:
         raise MoeError(rc, "moe_bias_update")
+
+
+# ---------------------------------------------------------------- around the expert layer
+
+
+def _rows(t: Optional[torch.Tensor], name: str, dtype, T: int, cols: int):
+    """(pointer, row stride) of [T][cols] activations: contiguous rows, any stride between them."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != cols:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, cols)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    # the stride of a dimension of one is arbitrary
+    return t.data_ptr(), ld if T > 1 else max(cols, 1)
+
+
+def _packed(t: Optional[torch.Tensor], name: str, dtype, *shape):
+    """Pointer to a packed tensor of this shape, or None."""
+    if t is None:
+        return None
+    _check(t, name, dtype, shape)
+    return t.data_ptr()
+
+
+def _need(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} is required")
+
+
+def _ws(ws: Optional[torch.Tensor]):
+    """(pointer, bytes) of a workspace: any contiguous device tensor."""
+    if ws is None:
+        return None, 0
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous device tensor")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _alloc(name: str, cfg, T: int, device) -> torch.Tensor:
+    n = int(getattr(lib(), f"moe_{name}_workspace_bytes")(ctypes.byref(cfg), int(T)))
+    if n == 0 and T > 0:
+        raise MoeError(-2, f"moe_{name}_workspace_bytes")
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+
+
+def _call(name: str, *args) -> None:
+    rc = getattr(lib(), name)(*args)
+    if rc != 0:
+        raise MoeError(rc, name)
+
+
+def make_norm_cfg(hidden: int, dtype=BF16, kind: str = "rms", gate_rows: int = 0,
+                  eps: float = 1e-6, res_scale: float = 1.0) -> _NormCfg:
+    """moe_norm_cfg; gate_rows: consecutive tokens that share a row of the gate (0: no gate)."""
+    return _NormCfg(hidden, _DT_NAME.get(dtype, dtype), _NORM_KIND.get(kind, kind), gate_rows, eps,
+                    res_scale)
+
+
+def _norm_params(cfg: _NormCfg, T: int, dt, params: Dict[str, Optional[torch.Tensor]]):
+    H, n = cfg.hidden, cfg.gate_rows
+    vec = [_packed(params.get(k), k, dt, H) for k in ("w_post", "b_post", "w_pre", "b_pre")]
+    return _NormParams(*vec, _packed(params.get("gate"), "gate", dt, T // n if n > 0 else 0, H))
+
+
+def norm_forward(cfg: _NormCfg, residual: torch.Tensor, branch: Optional[torch.Tensor],
+                 params: Dict[str, Optional[torch.Tensor]], u: Optional[torch.Tensor],
+                 h: Optional[torch.Tensor], stream=None) -> None:
+    """moe_norm_forward: u = s residual + gate post(branch), h = pre(u).
+
+    ``params``: w_post, b_post, w_pre, b_pre ([hidden]) and gate ([T / gate_rows][hidden]); absent
+    or None ones as in ``include/moe.h``.  ``u`` or ``h`` may be None."""
+    _need(residual=residual)
+    T, H, dt = residual.shape[0], cfg.hidden, _TORCH_DT[cfg.dtype]
+    p = _norm_params(cfg, T, dt, params)
+    _call("moe_norm_forward", cfg, T, *_rows(residual, "residual", dt, T, H),
+          *_rows(branch, "branch", dt, T, H), p, *_rows(u, "u", dt, T, H), *_rows(h, "h", dt, T, H),
+          _stream(stream))
+
+
+def norm_backward_workspace_bytes(cfg: _NormCfg, T: int) -> int:
+    return int(lib().moe_norm_backward_workspace_bytes(ctypes.byref(cfg), int(T)))
+
+
+def alloc_norm_backward_workspace(cfg: _NormCfg, T: int, device="cuda") -> torch.Tensor:
+    return _alloc("norm_backward", cfg, T, device)
+
+
+def norm_backward(cfg: _NormCfg, residual: torch.Tensor, branch: Optional[torch.Tensor],
+                  params: Dict[str, Optional[torch.Tensor]], du: Optional[torch.Tensor],
+                  dh: Optional[torch.Tensor], grads: Dict[str, torch.Tensor], ws: torch.Tensor,
+                  stream=None) -> None:
+    """moe_norm_backward: gradients of <du, u> + <dh, h> into the tensors of ``grads``
+    (residual, branch, w_post, b_post, w_pre, b_pre, gate; those absent are not formed)."""
+    _need(residual=residual)
+    T, H, n, dt = residual.shape[0], cfg.hidden, cfg.gate_rows, _TORCH_DT[cfg.dtype]
+    p = _norm_params(cfg, T, dt, params)
+    vec = [_packed(grads.get(k), f"grads[{k}]", dt, H) for k in ("w_post", "b_post", "w_pre", "b_pre")]
+    g = _NormGrads(*_rows(grads.get("residual"), "grads[residual]", dt, T, H),
+                   *_rows(grads.get("branch"), "grads[branch]", dt, T, H), *vec,
+                   _packed(grads.get("gate"), "grads[gate]", dt, T // n if n > 0 else 0, H))
+    _call("moe_norm_backward", cfg, T, *_rows(residual, "residual", dt, T, H),
+          *_rows(branch, "branch", dt, T, H), p, *_rows(du, "du", dt, T, H),
+          *_rows(dh, "dh", dt, T, H), g, *_ws(ws), _stream(stream))
+
+
+def make_linear_cfg(in_dim: int, out_dim: int, act: str = "none", dtype=BF16) -> _LinearCfg:
+    """moe_linear_cfg; act: "none", "relu", "silu" or "gelu"."""
+    return _LinearCfg(in_dim, out_dim, _ACT.get(act, act), _DT_NAME.get(dtype, dtype))
+
+
+def linear_workspace_bytes(cfg: _LinearCfg, T: int) -> int:
+    return int(lib().moe_linear_workspace_bytes(ctypes.byref(cfg), int(T)))
+
+
+def linear_backward_workspace_bytes(cfg: _LinearCfg, T: int) -> int:
+    return int(lib().moe_linear_backward_workspace_bytes(ctypes.byref(cfg), int(T)))
+
+
+def alloc_linear_workspace(cfg: _LinearCfg, T: int, device="cuda") -> torch.Tensor:
+    return _alloc("linear", cfg, T, device)
+
+
+def alloc_linear_backward_workspace(cfg: _LinearCfg, T: int, device="cuda") -> torch.Tensor:
+    return _alloc("linear_backward", cfg, T, device)
+
+
+def linear_forward(cfg: _LinearCfg, x: torch.Tensor, w: torch.Tensor, y: torch.Tensor,
+                   ws: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                   residual: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_linear_forward: y = residual + act(x w^T + bias)."""
+    _need(x=x, w=w, y=y)
+    T, K, N, dt = x.shape[0], cfg.in_dim, cfg.out_dim, _TORCH_DT[cfg.dtype]
+    _call("moe_linear_forward", cfg, T, *_rows(x, "x", dt, T, K), _packed(w, "w", dt, N, K),
+          _packed(bias, "bias", dt, N), *_rows(residual, "residual", dt, T, N),
+          *_rows(y, "y", dt, T, N), *_ws(ws), _stream(stream))
+
+
+def linear_backward(cfg: _LinearCfg, x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor,
+                    ws: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                    dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                    dbias: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_linear_backward: gradients of <dy, y> into those of dx, dw and dbias that are given."""
+    _need(x=x, w=w, dy=dy)
+    T, K, N, dt = x.shape[0], cfg.in_dim, cfg.out_dim, _TORCH_DT[cfg.dtype]
+    _call("moe_linear_backward", cfg, T, *_rows(x, "x", dt, T, K), _packed(w, "w", dt, N, K),
+          _packed(bias, "bias", dt, N), *_rows(dy, "dy", dt, T, N), *_rows(dx, "dx", dt, T, K),
+          _packed(dw, "dw", dt, N, K), _packed(dbias, "dbias", dt, N), *_ws(ws), _stream(stream))
+
+
+def make_ffn_cfg(hidden: int, inter: int, act: str = "silu", dtype=BF16) -> _FfnCfg:
+    """moe_ffn_cfg; act: "silu", "gelu" or "relu"."""
+    return _FfnCfg(hidden, inter, _ACT.get(act, act), _DT_NAME.get(dtype, dtype))
+
+
+def ffn_workspace_bytes(cfg: _FfnCfg, T: int) -> int:
+    return int(lib().moe_ffn_workspace_bytes(ctypes.byref(cfg), int(T)))
+
+
+def ffn_backward_workspace_bytes(cfg: _FfnCfg, T: int) -> int:
+    return int(lib().moe_ffn_backward_workspace_bytes(ctypes.byref(cfg), int(T)))
+
+
+def alloc_ffn_workspace(cfg: _FfnCfg, T: int, device="cuda") -> torch.Tensor:
+    return _alloc("ffn", cfg, T, device)
+
+
+def alloc_ffn_backward_workspace(cfg: _FfnCfg, T: int, device="cuda") -> torch.Tensor:
+    return _alloc("ffn_backward", cfg, T, device)
+
+
+def _ffn_weights(cfg: _FfnCfg, dt, w: Dict[str, torch.Tensor]):
+    H, I = cfg.hidden, cfg.inter
+    _need(**{k: w.get(k) for k in ("w_gate", "w_up", "w_down")})
+    return (_packed(w["w_gate"], "w_gate", dt, I, H), _packed(w["w_up"], "w_up", dt, I, H),
+            _packed(w["w_down"], "w_down", dt, H, I))
+
+
+def ffn_forward(cfg: _FfnCfg, x: torch.Tensor, weights: Dict[str, torch.Tensor], y: torch.Tensor,
+                ws: torch.Tensor, residual: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_ffn_forward: y = residual + (act(x w_gate^T) * (x w_up^T)) w_down^T."""
+    _need(x=x, y=y)
+    T, H, dt = x.shape[0], cfg.hidden, _TORCH_DT[cfg.dtype]
+    _call("moe_ffn_forward", cfg, T, *_rows(x, "x", dt, T, H), *_ffn_weights(cfg, dt, weights),
+          *_rows(residual, "residual", dt, T, H), *_rows(y, "y", dt, T, H), *_ws(ws),
+          _stream(stream))
+
+
+def ffn_backward(cfg: _FfnCfg, x: torch.Tensor, weights: Dict[str, torch.Tensor],
+                 dy: torch.Tensor, dx: torch.Tensor, dw_gate: torch.Tensor, dw_up: torch.Tensor,
+                 dw_down: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """moe_ffn_backward: gradients of <dy, y> into dx and the weight gradients."""
+    _need(x=x, dy=dy, dx=dx, dw_gate=dw_gate, dw_up=dw_up, dw_down=dw_down)
+    T, H, I, dt = x.shape[0], cfg.hidden, cfg.inter, _TORCH_DT[cfg.dtype]
+    _call("moe_ffn_backward", cfg, T, *_rows(x, "x", dt, T, H), *_ffn_weights(cfg, dt, weights),
+          *_rows(dy, "dy", dt, T, H), *_rows(dx, "dx", dt, T, H),
+          _packed(dw_gate, "dw_gate", dt, I, H), _packed(dw_up, "dw_up", dt, I, H),
+          _packed(dw_down, "dw_down", dt, H, I), *_ws(ws), _stream(stream))

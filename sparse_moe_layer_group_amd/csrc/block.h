@@ -1,0 +1,199 @@
+// Shared pieces of the operators around the expert layer (norm_kernels.hip,
+// dense_gemm.hip, dense_stream.hip, block_api.cpp); not part of the C ABI.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+// ---------------------------------------------------------------- activations
+
+// codes of enum moe_act
+constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3;
+
+// act(z), float32; GELU is z Phi(z) with the error function
+MOE_DEV float act_value(int act, float z) {
+  if (act == kActSilu) return siluf(z);
+  if (act == kActGelu) return 0.5f * z * erfcf(-0.70710678118654752f * z);
+  if (act == kActRelu) return fmaxf(z, 0.f);
+  return z;
+}
+
+// act'(z)
+MOE_DEV float act_slope(int act, float z) {
+  if (act == kActSilu) {
+    const float s = sigmoidf(z);
+    return s * (1.0f + z * (1.0f - s));
+  }
+  if (act == kActGelu)  // Phi(z) + z phi(z)
+    return 0.5f * erfcf(-0.70710678118654752f * z) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+  if (act == kActRelu) return z > 0.f ? 1.f : 0.f;
+  return 1.f;
+}
+
+// ---------------------------------------------------------------- 8 elements of a row
+
+// Global memory takes vector accesses at any element's address; these types
+// let the compiler use them where a row's start is aligned to its element only.
+struct __attribute__((packed, aligned(2))) u32x4_at2 { u32x4 v; };
+struct __attribute__((packed, aligned(4))) f32x4_at4 { f32x4 v; };
+
+// Elements c .. c+7 of a row of n, zeros past its end.  WHOLE: n is a multiple
+// of 8, so eight elements are all inside the row or all past it.
+template <bool WHOLE> MOE_DEV void load8(const float* row, int c, int n, float (&v)[8]) {
+  if (c + 8 <= n) {
+    const f32x4 a = reinterpret_cast<const f32x4_at4*>(row + c)->v;
+    const f32x4 b = reinterpret_cast<const f32x4_at4*>(row + c + 4)->v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = !WHOLE && c + i < n ? row[c + i] : 0.f;
+  }
+}
+MOE_DEV void unpack8(u32x4 a, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(a[i] << 16);
+    v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+  }
+}
+// the bfloat16 elements as they are, two to a register
+template <bool WHOLE> MOE_DEV u32x4 load8_raw(const bf16_t* row, int c, int n) {
+  if (c + 8 <= n) return reinterpret_cast<const u32x4_at2*>(row + c)->v;
+  u32x4 a = {0u, 0u, 0u, 0u};
+  if (!WHOLE && c < n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = c + 2 * i < n ? row[c + 2 * i] : 0u, hi = c + 2 * i + 1 < n ? row[c + 2 * i + 1] : 0u;
+      a[i] = lo | (hi << 16);
+    }
+  }
+  return a;
+}
+template <bool WHOLE> MOE_DEV void load8(const bf16_t* row, int c, int n, float (&v)[8]) {
+  unpack8(load8_raw<WHOLE>(row, c, n), v);
+}
+
+// two float32 to a pair of bfloat16, round to nearest even (gfx950's v_cvt_pk_bf16_f32)
+MOE_DEV uint32_t pack_bf16(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 p = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, p);
+}
+MOE_DEV u32x4 pack8(const float (&v)[8]) {
+  return u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+}
+
+template <bool WHOLE> MOE_DEV void store8(float* row, int c, int n, const float (&v)[8]) {
+  if (c + 8 <= n) {
+    reinterpret_cast<f32x4_at4*>(row + c)->v = f32x4{v[0], v[1], v[2], v[3]};
+    reinterpret_cast<f32x4_at4*>(row + c + 4)->v = f32x4{v[4], v[5], v[6], v[7]};
+  } else if (!WHOLE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < n) row[c + i] = v[i];
+  }
+}
+template <bool WHOLE> MOE_DEV void store8(bf16_t* row, int c, int n, const float (&v)[8]) {
+  if (c + 8 <= n) {
+    reinterpret_cast<u32x4_at2*>(row + c)->v = pack8(v);
+  } else if (!WHOLE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < n) row[c + i] = f32_to_bf16(v[i]);
+  }
+}
+
+// sum over the wave in a fixed order, every lane gets it: lane moves within
+// 16-lane rows by DPP, the last two steps by shuffles
+template <int CTRL> MOE_DEV float add_dpp(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
+}
+MOE_DEV float wave_total(float v) {
+  v = add_dpp<0xb1>(v);   // lane ^ 1
+  v = add_dpp<0x4e>(v);   // lane ^ 2
+  v = add_dpp<0x124>(v);  // row_ror:4
+  v = add_dpp<0x128>(v);  // row_ror:8
+  v += __shfl_xor(v, 16, kWave);
+  v += __shfl_xor(v, 32, kWave);
+  return v;
+}
+
+// ---------------------------------------------------------------- norm (norm_kernels.hip)
+
+// One call's arguments; row strides in elements.  Absent tensors are NULL.
+struct NormArgs {
+  const void *residual, *branch, *du, *dh;
+  const void *w_post, *b_post, *w_pre, *b_pre, *gate;
+  void *u, *h;                       // forward outputs
+  void *d_residual, *d_branch;       // backward outputs
+  void *dw_post, *db_post, *dw_pre, *db_pre, *dgate;
+  float* part;                       // [4][workers][H]: per-worker sums of dw_post, db_post, dw_pre, db_pre
+  float* gpart;                      // [2 workers][H]: of the gate rows that workers share
+  int64_t ld_residual, ld_branch, ld_u, ld_h, ld_du, ld_dh, ld_dr, ld_db;
+  int64_t T;
+  int H, gate_rows, layer;           // gate_rows 0: no gate
+  int workers, options;              // set by the launchers
+  float eps, scale;
+};
+int norm_backward_workers(int64_t T, int H);
+hipError_t launch_norm_forward(const NormArgs& a, bool bf16, hipStream_t st);
+hipError_t launch_norm_backward(const NormArgs& a, bool bf16, hipStream_t st);
+constexpr int kNormMaxHidden = 16384;
+
+// ---------------------------------------------------------------- dense products (dense_gemm.hip)
+
+// What becomes of a product's float32 sums v (and u, the second product of a
+// dual call), 8 columns of a row at a time.
+enum DenseEpiMode {
+  kEpiOut = 0,    // out = residual + act(v + bias)
+  kEpiGated,      // p0 = act(v) u
+  kEpiKeep,       // g = v, u = u (float32)
+  kEpiGatedBack,  // v = dM: p0 = dM u act'(g), p1 = dM act(g), p2 = act(g) u
+  kEpiActBack     // p0 = dy act'(v + bias)
+};
+struct DenseEpi {
+  int mode, act, f32;       // f32: bias, residual, out and dy are float32 (else bfloat16)
+  int64_t M;
+  int N;                    // output columns
+  const void *bias, *residual, *dy;
+  void* out;
+  int64_t ld_residual, ld_out, ld_dy;
+  bf16_t *p0, *p1, *p2;     // staged operands: [f32 ? 3 : 1][M][ld_p], columns N .. ld_p up to 8 written as 0
+  int64_t plane, ld_p;      // elements between planes, and rows
+  float *g, *u;             // [M][ld_p]
+};
+
+// out[m][n] = sum over segments and k of A[m][k] B[n][k], each operand given
+// per segment.  Layout: a k-contiguous operand is [rows][ld], a k-slow one
+// [k][ld].  Operands are bfloat16, 16-byte aligned, ld % 8 == 0, and a
+// k-contiguous one holds zeros from K up to the next multiple of 8.
+constexpr int kMaxSegments = 12;
+enum DenseLayout { kNT = 0, kNN = 1, kTN = 2 };  // A, B: k-contiguous (N... T) as in A B^T, A B, A^T B
+struct DenseArgs {
+  const bf16_t* a[kMaxSegments];
+  const bf16_t* b[kMaxSegments];
+  const bf16_t* b2[kMaxSegments];  // dual (kNT only): the second product's B
+  int64_t lda, ldb;
+  int64_t M, K;                    // K of one segment
+  int N, segments, dual;
+  int split, steps_per_split;      // set by the launcher
+  float* part;                     // split > 1: [split][1 + dual][M][ld_part]
+  int64_t ld_part;
+  DenseEpi epi;
+};
+size_t dense_part_bytes(int layout, int64_t M, int N, int64_t K, int segments, int dual);
+hipError_t launch_dense(const DenseArgs& a, int layout, hipStream_t st);
+
+// planes of an operand: dst [f32 ? 3 : 1][rows][ld_dst] with zeros past cols.
+// float32 values are split exactly into three bfloat16 parts.
+hipError_t launch_dense_pack(const void* src, int64_t ld_src, bool f32, int64_t rows, int cols, bf16_t* dst,
+                             int64_t ld_dst, hipStream_t st);
+
+// out[n] = sum over rows of src[r][n]; planes as above (n_planes 1 or 3) or, n_planes 0, float32
+size_t dense_colsum_bytes(int64_t rows, int cols);
+hipError_t launch_dense_colsum(const void* src, int64_t ld, int n_planes, int64_t plane, int64_t rows, int cols,
+                               void* out, bool f32, float* part, hipStream_t st);
+
+}  // namespace moe

@@ -1,0 +1,581 @@
+// Norms after a block and before the next one, fused with the gate and the
+// residual stream between them.
+//
+//   p = unit(f), n = p w_post + b_post, u = s r + gate n, q = unit(u),
+//   h = q w_pre + b_pre, unit(v) = (v - m) / sqrt(mean((v - m)^2) + eps)
+// with m the row's mean (layer norm) or 0 (RMS norm), r the residual stream
+// and f the block's output.  All in float32, rounded once at each store; the
+// mean is taken out before the squares are summed, so a row far from zero
+// loses nothing.
+//
+// Backward of <du, u> + <dh, h>, from r and f again (nothing is kept from the
+// forward):
+//   a = dh w_pre, e = du + (a - [mean a] - q mean(a q)) / sigma_u, dr = s e,
+//   dgate = sum e n, g = e gate, dw_post = sum g p, db_post = sum g,
+//   c = g w_post, df = (c - [mean c] - p mean(c p)) / sigma_f,
+//   dw_pre = sum dh q, db_pre = sum dh
+// ([.] for the layer norm).
+//
+// Memory-bound: 4 (forward) or 6 (backward) rows move per token and about 14
+// or 40 operations an element.  A row therefore stays in registers from its
+// load to its stores, 8 consecutive elements a thread, so every element is
+// read and written once however many statistics the row needs.  A row of up
+// to 1024 is one wave's, and needs no barrier; a longer row is one
+// workgroup's, of as many waves as it has 512s.  A worker (that wave or
+// workgroup) takes a contiguous range of rows: it keeps the norm weights in
+// registers over them, has its next row's loads in flight while it works on
+// the present one, and in the backward adds its columns' weight gradients up
+// in registers, one partial row a worker, which a second kernel joins in
+// worker order (deterministic, no atomics).
+#include "block.h"
+
+namespace moe {
+
+namespace {
+
+// Row sums over the worker's threads.  ONE_WAVE: the wave alone.  Else each
+// wave leaves its sum in LDS and every thread adds them in wave order; three
+// alternating slots make one barrier per sum enough (a wave can be at most one
+// sum ahead of the slowest, which has read the slot before last).
+struct RowSum {
+  float* lds;  // [3][2][16]
+  int nwave, turn;
+  template <bool ONE_WAVE> MOE_DEV void sum2(float& a, float& b) {
+    a = wave_total(a);
+    b = wave_total(b);
+    if (ONE_WAVE) return;
+    float* s = lds + turn * 32;
+    turn = turn == 2 ? 0 : turn + 1;
+    if ((threadIdx.x & 63) == 0) {
+      s[threadIdx.x >> 6] = a;
+      s[16 + (threadIdx.x >> 6)] = b;
+    }
+    __syncthreads();
+    a = 0.f;
+    b = 0.f;
+    for (int w = 0; w < nwave; ++w) {
+      a += s[w];
+      b += s[16 + w];
+    }
+  }
+  template <bool ONE_WAVE> MOE_DEV float sum(float v) {
+    v = wave_total(v);
+    if (ONE_WAVE) return v;
+    float* s = lds + turn * 32;
+    turn = turn == 2 ? 0 : turn + 1;
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.f;
+    for (int w = 0; w < nwave; ++w) v += s[w];
+    return v;
+  }
+};
+
+// raw (unconverted) 8 elements of a row, so that a row in flight costs its own
+// bytes in registers
+template <typename TE, bool WHOLE> struct Raw8;
+template <bool WHOLE> struct Raw8<bf16_t, WHOLE> {
+  typedef bf16_t TE;
+  u32x4 a;
+  MOE_DEV void load(const bf16_t* row, int c, int n) { a = load8_raw<WHOLE>(row, c, n); }
+  MOE_DEV void fill(bool one) { a = u32x4{1u, 1u, 1u, 1u} * (one ? 0x3f803f80u : 0u); }
+  // what is made of the value is made anew behind this point: without it the
+  // float32 forms of a row's parameters, twice as many registers, are kept
+  // over the worker's rows in place of the packed ones
+  MOE_DEV void pin() { asm volatile("" : "+v"(a)); }
+  MOE_DEV void get(float (&v)[8]) const { unpack8(a, v); }
+};
+template <bool WHOLE> struct Raw8<float, WHOLE> {
+  typedef float TE;
+  f32x4 a, b;
+  MOE_DEV void load(const float* row, int c, int n) {
+    float v[8];
+    load8<WHOLE>(row, c, n, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { a[i] = v[i]; b[i] = v[4 + i]; }
+  }
+  MOE_DEV void fill(bool one) { a = b = f32x4{1.f, 1.f, 1.f, 1.f} * (one ? 1.f : 0.f); }
+  MOE_DEV void pin() {}
+  MOE_DEV void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
+  }
+};
+
+// v becomes the unit row (0 past the row's end); returns 1 / sigma
+template <class S>
+MOE_DEV float unit_row(float (&v)[S::NV][8], const int (&c)[S::NV], int H, float eps, RowSum& rs) {
+  constexpr int NV = S::NV;
+  constexpr bool ONE_WAVE = S::ONE_WAVE;
+  const float rh = 1.0f / float(H);
+  if (S::LAYER) {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[j][i];
+    const float m = rs.sum<ONE_WAVE>(s) * rh;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] = c[j] + i < H ? v[j][i] - m : 0.f;
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
+  const float inv = 1.0f / sqrtf(rs.sum<ONE_WAVE>(ss) * rh + eps);
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[j][i] *= inv;
+  return inv;
+}
+
+template <class R> MOE_DEV void take(R& r, const void* p, int c, int H, bool one) {
+  if (p) r.load(static_cast<const typename R::TE*>(p), c, H);
+  else r.fill(one);
+}
+
+// v w, or v w + b
+template <class S, class R> MOE_DEV void affine(float (&v)[8], const R& weight, const R& bias) {
+  float w[8], b[8];
+  weight.get(w);
+  if (S::LAYER) bias.get(b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = S::LAYER ? fmaf(v[i], w[i], b[i]) : v[i] * w[i];
+}
+
+// first row of worker w of n over T rows
+MOE_DEV int64_t worker_row(int64_t T, int w, int n) { return T * w / n; }
+
+// NV: vectors of 8 a thread; LAYER: layer norm; WHOLE: H % 8 == 0
+template <typename TE_, int NV_, bool ONE_WAVE_, bool LAYER_, bool WHOLE_> struct NormShape {
+  typedef TE_ TE;
+  static constexpr int NV = NV_;
+  static constexpr bool ONE_WAVE = ONE_WAVE_, LAYER = LAYER_, WHOLE = WHOLE_;
+};
+
+// NormArgs::options, set by the launchers from the pointers given
+constexpr int kNormPost = 1, kNormGate = 2, kNormU = 4, kNormPre = 8, kNormDResidual = 16, kNormDBranch = 32;
+
+int norm_options(const NormArgs& a) {
+  return (a.branch && a.w_post ? kNormPost : 0) | (a.gate_rows ? kNormGate : 0) | (a.u ? kNormU : 0) |
+         (a.h || a.dh ? kNormPre : 0) | (a.d_residual ? kNormDResidual : 0) | (a.d_branch ? kNormDBranch : 0);
+}
+
+constexpr int kRowThreads = 512;  // most threads of a workgroup that shares a row
+constexpr int kRowWaves = 4;  // waves (one row each) of a workgroup of one-wave workers
+
+}  // namespace
+
+// ---------------------------------------------------------------- forward
+
+template <class S>
+__global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kRowThreads) void norm_forward_kernel(NormArgs a) {
+  typedef typename S::TE TE;
+  constexpr int NV = S::NV;
+  constexpr bool ONE = S::ONE_WAVE;
+  __shared__ float lds[96];
+  const int H = a.H;
+  const int tid = ONE ? threadIdx.x & 63 : threadIdx.x;
+  const int nthr = ONE ? 64 : blockDim.x;
+  const int worker = ONE ? blockIdx.x * kRowWaves + (threadIdx.x >> 6) : blockIdx.x;
+  if (worker >= a.workers) return;  // whole waves, and no barrier below for them
+  RowSum rs{lds, int(blockDim.x >> 6), 0};
+  int c[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) c[j] = (j * nthr + tid) * 8;
+
+  const TE* r = static_cast<const TE*>(a.residual);
+  const TE* f = static_cast<const TE*>(a.branch);
+  // absent parameters are ones or zeros: the arithmetic is the same
+  typedef Raw8<TE, S::WHOLE> Raw;
+  Raw wpost[NV], wpre[NV], gate[NV], bpost[S::LAYER ? NV : 1], bpre[S::LAYER ? NV : 1];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    take(wpost[j], a.w_post, c[j], H, true);
+    take(wpre[j], a.w_pre, c[j], H, true);
+    gate[j].fill(true);
+    if (S::LAYER) {
+      take(bpost[j], a.b_post, c[j], H, false);
+      take(bpre[j], a.b_pre, c[j], H, false);
+    }
+  }
+  const int64_t t0 = worker_row(a.T, worker, a.workers), t1 = worker_row(a.T, worker + 1, a.workers);
+  int64_t group_end = t0;
+  Raw rn[NV], fn[NV];
+  auto fetch = [&](int64_t t) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      rn[j].load(r + t * a.ld_residual, c[j], H);
+      if (f) fn[j].load(f + t * a.ld_branch, c[j], H);
+      else fn[j].fill(false);
+    }
+  };
+  if (t0 < t1) fetch(t0);
+  for (int64_t t = t0; t < t1; ++t) {
+    // The options are read anew for every row: the loop is not to be cloned
+    // for each combination of them.
+    int opt = a.options;
+    asm volatile("" : "+s"(opt));
+    if ((opt & kNormGate) && t >= group_end) {
+      const int64_t group = t / a.gate_rows;
+      group_end = (group + 1) * a.gate_rows;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) gate[j].load(static_cast<const TE*>(a.gate) + group * H, c[j], H);
+    }
+    float u[NV][8], v[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      rn[j].get(u[j]);
+      fn[j].get(v[j]);
+      wpost[j].pin();
+      wpre[j].pin();
+      gate[j].pin();
+    }
+    if (t + 1 < t1) fetch(t + 1);
+    if (opt & kNormPost) {
+      unit_row<S>(v, c, H, a.eps, rs);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) affine<S>(v[j], wpost[j], bpost[S::LAYER ? j : 0]);
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float g[8];
+      gate[j].get(g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[j][i] = fmaf(v[j][i], g[i], a.scale * u[j][i]);
+      if (opt & kNormU) store8<S::WHOLE>(static_cast<TE*>(a.u) + t * a.ld_u, c[j], H, u[j]);
+    }
+    if (opt & kNormPre) {
+      unit_row<S>(u, c, H, a.eps, rs);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        affine<S>(u[j], wpre[j], bpre[S::LAYER ? j : 0]);
+        store8<S::WHOLE>(static_cast<TE*>(a.h) + t * a.ld_h, c[j], H, u[j]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- backward
+
+// The gate row's gradient goes straight to its place where the worker has all
+// of the row's tokens.  A gate row that several workers share is joined from
+// their partial rows: gpart[2 w] is worker w's share of a row begun before its
+// range, gpart[2 w + 1] of one begun inside it and going on after it.
+template <class S>
+__global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kRowThreads) void norm_backward_kernel(NormArgs a) {
+  typedef typename S::TE TE;
+  constexpr int NV = S::NV;
+  constexpr bool ONE = S::ONE_WAVE;
+  __shared__ float lds[96];
+  const int H = a.H;
+  const float rh = 1.0f / float(H);
+  const int tid = ONE ? threadIdx.x & 63 : threadIdx.x;
+  const int nthr = ONE ? 64 : blockDim.x;
+  const int worker = ONE ? blockIdx.x * kRowWaves + (threadIdx.x >> 6) : blockIdx.x;
+  if (worker >= a.workers) return;
+  RowSum rs{lds, int(blockDim.x >> 6), 0};
+  int c[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) c[j] = (j * nthr + tid) * 8;
+
+  const TE* r = static_cast<const TE*>(a.residual);
+  const TE* f = static_cast<const TE*>(a.branch);
+  const TE* du = static_cast<const TE*>(a.du);
+  const TE* dh = static_cast<const TE*>(a.dh);
+  typedef Raw8<TE, S::WHOLE> Raw;
+  constexpr int NB = S::LAYER ? NV : 1;  // vectors of what only the layer norm has
+  Raw wpost[NV], wpre[NV], gate[NV], bpost[NB];
+  float swpost[NV][8], swpre[NV][8], sgate[NV][8], sbpost[NB][8], sbpre[NB][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    take(wpost[j], a.w_post, c[j], H, true);
+    take(wpre[j], a.w_pre, c[j], H, true);
+    gate[j].fill(true);
+    if (S::LAYER) take(bpost[j], a.b_post, c[j], H, false);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      swpost[j][i] = swpre[j][i] = sgate[j][i] = 0.f;
+      if (S::LAYER) sbpost[j][i] = sbpre[j][i] = 0.f;
+    }
+  }
+
+  const int64_t t0 = worker_row(a.T, worker, a.workers), t1 = worker_row(a.T, worker + 1, a.workers);
+  int64_t group = -1, group_end = t0;
+  // the gate row `group` ends at row `end` of the worker's range
+  auto flush_gate = [&](int64_t end) {
+    if (a.dgate == nullptr || group < 0) return;
+    const int64_t first = group * a.gate_rows, last = first + a.gate_rows;
+    const bool whole = first >= t0 && last <= end;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (whole) store8<S::WHOLE>(static_cast<TE*>(a.dgate) + group * H, c[j], H, sgate[j]);
+      else store8<S::WHOLE>(a.gpart + (2 * int64_t(worker) + (first >= t0 ? 1 : 0)) * H, c[j], H, sgate[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sgate[j][i] = 0.f;
+    }
+  };
+  Raw rn[NV], fn[NV], dun[NV], dhn[NV];
+  auto fetch = [&](int64_t t) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      rn[j].load(r + t * a.ld_residual, c[j], H);
+      if (f) fn[j].load(f + t * a.ld_branch, c[j], H);
+      else fn[j].fill(false);
+      if (du) dun[j].load(du + t * a.ld_du, c[j], H);
+      else dun[j].fill(false);
+      if (dh) dhn[j].load(dh + t * a.ld_dh, c[j], H);
+      else dhn[j].fill(false);
+    }
+  };
+  if (t0 < t1) fetch(t0);
+  for (int64_t t = t0; t < t1; ++t) {
+    int opt = a.options;  // read anew for every row, as in the forward
+    asm volatile("" : "+s"(opt));
+    if ((opt & kNormGate) && t >= group_end) {
+      flush_gate(t);
+      group = t / a.gate_rows;
+      group_end = (group + 1) * a.gate_rows;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) gate[j].load(static_cast<const TE*>(a.gate) + group * H, c[j], H);
+    }
+    float q[NV][8], p[NV][8], e[NV][8], d[NV][8];  // u, then q; p; du, then e; dh, then a
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      rn[j].get(q[j]);
+      fn[j].get(p[j]);
+      dun[j].get(e[j]);
+      dhn[j].get(d[j]);
+      wpost[j].pin();
+      wpre[j].pin();
+      gate[j].pin();
+    }
+    if (t + 1 < t1) fetch(t + 1);
+    float inv_f = 1.f;
+    if (opt & kNormPost) inv_f = unit_row<S>(p, c, H, a.eps, rs);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float n[8], g[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n[i] = p[j][i];
+      affine<S>(n, wpost[j], bpost[S::LAYER ? j : 0]);
+      gate[j].get(g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[j][i] = fmaf(n[i], g[i], a.scale * q[j][i]);
+    }
+    if (opt & kNormPre) {
+      const float inv_u = unit_row<S>(q, c, H, a.eps, rs);
+      float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float w[8];
+        wpre[j].get(w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          swpre[j][i] = fmaf(d[j][i], q[j][i], swpre[j][i]);
+          if (S::LAYER) sbpre[j][i] += d[j][i];
+          d[j][i] *= w[i];
+          if (S::LAYER) s1 += d[j][i];
+          s2 = fmaf(d[j][i], q[j][i], s2);
+        }
+      }
+      if (S::LAYER) rs.template sum2<ONE>(s1, s2);
+      else s2 = rs.template sum<ONE>(s2);
+      s1 *= rh;
+      s2 *= rh;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[j][i] = fmaf(inv_u, d[j][i] - s1 - q[j][i] * s2, e[j][i]);
+    }
+    // e is the gradient at u
+    float s3 = 0.f, s4 = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float w[8], g[8], n[8];
+      if (opt & kNormDResidual) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n[i] = a.scale * e[j][i];
+        store8<S::WHOLE>(static_cast<TE*>(a.d_residual) + t * a.ld_dr, c[j], H, n);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n[i] = p[j][i];
+      affine<S>(n, wpost[j], bpost[S::LAYER ? j : 0]);
+      gate[j].get(g);
+      wpost[j].get(w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sgate[j][i] = fmaf(e[j][i], n[i], sgate[j][i]);
+        e[j][i] *= g[i];
+        swpost[j][i] = fmaf(e[j][i], p[j][i], swpost[j][i]);
+        if (S::LAYER) sbpost[j][i] += e[j][i];
+        e[j][i] *= w[i];
+        if (S::LAYER) s3 += e[j][i];
+        s4 = fmaf(e[j][i], p[j][i], s4);
+      }
+    }
+    if (!(opt & kNormDBranch)) continue;
+    if (opt & kNormPost) {
+      if (S::LAYER) rs.template sum2<ONE>(s3, s4);
+      else s4 = rs.template sum<ONE>(s4);
+      s3 *= rh;
+      s4 *= rh;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[j][i] = inv_f * (e[j][i] - s3 - p[j][i] * s4);
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) store8<S::WHOLE>(static_cast<TE*>(a.d_branch) + t * a.ld_db, c[j], H, e[j]);
+  }
+  flush_gate(t1);
+  const int64_t plane = int64_t(a.workers) * H;
+  float* part = a.part + int64_t(worker) * H;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (a.dw_post) store8<S::WHOLE>(part, c[j], H, swpost[j]);
+    if (a.dw_pre) store8<S::WHOLE>(part + 2 * plane, c[j], H, swpre[j]);
+    if (S::LAYER) {
+      if (a.db_post) store8<S::WHOLE>(part + plane, c[j], H, sbpost[j]);
+      if (a.db_pre) store8<S::WHOLE>(part + 3 * plane, c[j], H, sbpre[j]);
+    }
+  }
+}
+
+// Joins the workers' partial rows in worker order: blockIdx.y 0..3 the weight
+// gradients, 4 + g the gate row g.  A workgroup has 64 columns and 16 shares
+// of the workers (share k: workers k, k + 16, ...), added up share by share.
+constexpr int kJoinShares = 16;
+template <typename TE>
+__global__ __launch_bounds__(64 * kJoinShares) void norm_join_kernel(NormArgs a) {
+  __shared__ float acc[kJoinShares][64];
+  const int lane = threadIdx.x & 63, share = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + lane;
+  const int64_t which = blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
+  TE* out;
+  const float* src;
+  int64_t first, last, step;
+  if (which < 4) {
+    void* const outs[4] = {a.dw_post, a.db_post, a.dw_pre, a.db_pre};
+    out = static_cast<TE*>(outs[which]);
+    src = a.part + which * a.workers * int64_t(a.H);
+    first = 0;
+    last = a.workers;
+    step = a.H;
+  } else {
+    const int64_t g = which - 4;
+    if (a.dgate == nullptr || g >= a.T / a.gate_rows) return;
+    const int64_t r0 = g * a.gate_rows, r1 = r0 + a.gate_rows;
+    // worker of row t: the largest w with T w / n <= t
+    first = ((r0 + 1) * a.workers - 1) / a.T;
+    last = (r1 * a.workers - 1) / a.T + 1;
+    if (last - first == 1) return;  // one worker had the whole row and wrote it
+    out = static_cast<TE*>(a.dgate) + g * a.H;
+    src = a.gpart;
+    step = 2 * int64_t(a.H);
+  }
+  if (out == nullptr) return;
+  float s = 0.f;
+  if (col < a.H) {
+#pragma unroll 4
+    for (int64_t w = first + share; w < last; w += kJoinShares)
+      s += src[w * step + (which >= 4 && w == first ? a.H : 0) + col];
+  }
+  acc[share][lane] = s;
+  __syncthreads();
+  if (share == 0 && col < a.H) {
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < kJoinShares; ++k) s += acc[k][lane];
+    out[col] = from_f32<TE>(s);
+  }
+}
+
+// ---------------------------------------------------------------- launches
+
+namespace {
+
+struct NormPlan {
+  bool one_wave;
+  int nv, threads;  // of a workgroup
+};
+NormPlan norm_plan(int H) {
+  if (H <= 1024) return {true, H <= 512 ? 1 : 2, 64 * kRowWaves};
+  const int nv = H <= 2 * 8 * kRowThreads ? 2 : 4;
+  return {false, nv, ((H + 8 * nv - 1) / (8 * nv) + 63) / 64 * 64};
+}
+static_assert(4 * 8 * kRowThreads >= kNormMaxHidden, "the widest row fits a workgroup");
+
+// F::launch<NormShape<...>> for the shape, kind and alignment of the call
+template <class F, typename TE, int NV, bool ONE> void pick_form(const NormArgs& a, const F& f) {
+  const bool whole = a.H % 8 == 0;
+  if (a.layer && whole) f(NormShape<TE, NV, ONE, true, true>{});
+  else if (a.layer) f(NormShape<TE, NV, ONE, true, false>{});
+  else if (whole) f(NormShape<TE, NV, ONE, false, true>{});
+  else f(NormShape<TE, NV, ONE, false, false>{});
+}
+template <class F, typename TE> void pick_shape(const NormArgs& a, const NormPlan& p, const F& f) {
+  if (p.one_wave && p.nv == 1) pick_form<F, TE, 1, true>(a, f);
+  else if (p.one_wave) pick_form<F, TE, 2, true>(a, f);
+  else if (p.nv == 2) pick_form<F, TE, 2, false>(a, f);
+  else pick_form<F, TE, 4, false>(a, f);
+}
+
+template <typename TE>
+hipError_t launch_forward(const NormArgs& a, const NormPlan& p, unsigned grid, hipStream_t st) {
+  auto f = [&](auto shape) {
+    hipLaunchKernelGGL((norm_forward_kernel<decltype(shape)>), dim3(grid), dim3(p.threads), 0, st, a);
+  };
+  pick_shape<decltype(f), TE>(a, p, f);
+  return hipGetLastError();
+}
+
+template <typename TE>
+hipError_t launch_backward(const NormArgs& a, const NormPlan& p, unsigned grid, hipStream_t st) {
+  auto f = [&](auto shape) {
+    hipLaunchKernelGGL((norm_backward_kernel<decltype(shape)>), dim3(grid), dim3(p.threads), 0, st, a);
+  };
+  pick_shape<decltype(f), TE>(a, p, f);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  const int64_t groups = a.dgate ? a.T / a.gate_rows : 0;
+  const int64_t jobs = 4 + groups;  // grid.y holds up to 65535 of them
+  const unsigned gy = unsigned(jobs < 32768 ? jobs : 32768), gz = unsigned((jobs + gy - 1) / gy);
+  hipLaunchKernelGGL((norm_join_kernel<TE>), dim3((a.H + 63) / 64, gy, gz), dim3(64 * kJoinShares), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// Workers of the backward: enough for every CU, few enough that their partial
+// rows stay small beside the tokens' own rows.
+int norm_backward_workers(int64_t T, int H) {
+  const int64_t most = H <= 1024 ? 1024 : 256;
+  return int(T < most ? T : most);
+}
+
+hipError_t launch_norm_forward(const NormArgs& args, bool bf16, hipStream_t st) {
+  NormArgs a = args;
+  a.options = norm_options(a);
+  const NormPlan p = norm_plan(a.H);
+  // every wave slot of the chip: workers hold their weights over their rows
+  const int64_t most = p.one_wave ? 256 * 32 : 256 * (2048 / p.threads);
+  a.workers = int(a.T < most ? a.T : most);
+  const unsigned grid = unsigned(p.one_wave ? (a.workers + kRowWaves - 1) / kRowWaves : a.workers);
+  return bf16 ? launch_forward<bf16_t>(a, p, grid, st) : launch_forward<float>(a, p, grid, st);
+}
+
+hipError_t launch_norm_backward(const NormArgs& args, bool bf16, hipStream_t st) {
+  NormArgs a = args;
+  a.options = norm_options(a);
+  const NormPlan p = norm_plan(a.H);
+  a.workers = norm_backward_workers(a.T, a.H);
+  const unsigned grid = unsigned(p.one_wave ? (a.workers + kRowWaves - 1) / kRowWaves : a.workers);
+  return bf16 ? launch_backward<bf16_t>(a, p, grid, st) : launch_backward<float>(a, p, grid, st);
+}
+
+}  // namespace moe
