@@ -11,24 +11,36 @@ namespace moe {
 // codes of enum moe_act
 constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3;
 
-// act(z), float32; GELU is z Phi(z) with the error function
-MOE_DEV float act_value(int act, float z) {
-  if (act == kActSilu) return siluf(z);
-  if (act == kActGelu) return 0.5f * z * erfcf(-0.70710678118654752f * z);
-  if (act == kActRelu) return fmaxf(z, 0.f);
-  return z;
+MOE_DEV float relu_value(float z) { return fmaxf(z, 0.f); }
+MOE_DEV float relu_slope(float z) { return z > 0.f ? 1.f : 0.f; }
+MOE_DEV float silu_slope(float z) {
+  const float s = sigmoidf(z);
+  return s * (1.0f + z * (1.0f - s));
+}
+// z Phi(z) and Phi(z) + z phi(z)
+MOE_DEV float gelu_value(float z) { return 0.5f * z * erfcf(-0.70710678118654752f * z); }
+MOE_DEV float gelu_slope(float z) {
+  return 0.5f * erfcf(-0.70710678118654752f * z) + z * 0.39894228040143268f * expf(-0.5f * z * z);
 }
 
-// act'(z)
-MOE_DEV float act_slope(int act, float z) {
-  if (act == kActSilu) {
-    const float s = sigmoidf(z);
-    return s * (1.0f + z * (1.0f - s));
-  }
-  if (act == kActGelu)  // Phi(z) + z phi(z)
-    return 0.5f * erfcf(-0.70710678118654752f * z) + z * 0.39894228040143268f * expf(-0.5f * z * z);
-  if (act == kActRelu) return z > 0.f ? 1.f : 0.f;
-  return 1.f;
+// eight values become their activation, or its slope there.  One branch on the
+// (uniform) kind for all eight: one for each keeps every kind's code in the way
+// of every element, and the instruction fetch of an epilogue then costs more
+// than its arithmetic.
+template <class F> MOE_DEV void each8(float (&v)[8], F f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = f(v[i]);
+}
+MOE_DEV void act_values(int act, float (&v)[8]) {
+  if (act == kActSilu) each8(v, siluf);
+  else if (act == kActGelu) each8(v, gelu_value);
+  else if (act == kActRelu) each8(v, relu_value);
+}
+MOE_DEV void act_slopes(int act, float (&v)[8]) {
+  if (act == kActSilu) each8(v, silu_slope);
+  else if (act == kActGelu) each8(v, gelu_slope);
+  else if (act == kActRelu) each8(v, relu_slope);
+  else each8(v, [](float) { return 1.f; });
 }
 
 // ---------------------------------------------------------------- 8 elements of a row

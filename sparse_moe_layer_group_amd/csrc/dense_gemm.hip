@@ -21,6 +21,8 @@
 // comparison and offsets stay small however large the matrix is; what lies
 // past the end of the contraction inside a k-contiguous row is masked by an
 // offset beyond every resource.
+#include <type_traits>
+
 #include "block.h"
 #include "lds_async.h"
 
@@ -38,8 +40,9 @@ typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) float lds_f32;
 typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 
-// s_waitcnt immediates: vmcnt(0) and lgkmcnt(0), vmcnt(0)
-constexpr int kWaitAll = 0x0070, kWaitCopies = 0x0f70;
+// s_waitcnt immediates: vmcnt(0) and lgkmcnt(0); vmcnt(n)
+constexpr int kWaitAll = 0x0070;
+constexpr int wait_copies(int n) { return (n & 15) | ((n >> 4) << 14) | 0x70 | 0xf00; }
 
 // position of 16-byte chunk c in k-row r: the four k-rows of one transposed
 // read hit distinct banks
@@ -67,14 +70,9 @@ template <int RL> MOE_DEV bf16x8 tr_frag(const bf16_t* st, int kbase, int i0, in
 
 // ---------------------------------------------------------------- epilogue
 
-MOE_DEV void load8_any(const void* p, bool f32, int64_t row, int64_t ld, int c, int n, float (&v)[8]) {
-  if (f32) load8<false>(static_cast<const float*>(p) + row * ld, c, n, v);
-  else load8<false>(static_cast<const bf16_t*>(p) + row * ld, c, n, v);
-}
-
-// v as staged planes at p (one, rounded to bfloat16; or three whose sum is v)
-MOE_DEV void store_planes(const DenseEpi& e, bf16_t* p, int64_t m, int n, const float (&v)[8]) {
-  bf16_t* at = p + m * e.ld_p + n;
+// v as staged planes at p + offset (one, rounded to bfloat16; or three whose sum is v)
+MOE_DEV void store_planes(const DenseEpi& e, bf16_t* p, int64_t offset, const float (&v)[8]) {
+  bf16_t* at = p + offset;
   if (!e.f32) {
     *reinterpret_cast<u32x4*>(at) = pack8(v);
     return;
@@ -102,71 +100,124 @@ MOE_DEV void store_f32(float* p, const float (&v)[8]) {
   reinterpret_cast<f32x4*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
 }
 
-// columns n .. n+7 (n % 8 == 0, n < N) of row m
-MOE_DEV void dense_epilogue(const DenseEpi& e, int64_t m, int n, float (&v)[8], float (&u)[8]) {
-  // sums of columns past N are of whatever lies there
+// columns n .. n+7 of rows m, m + step, ... of a matrix of the call's type.
+// INSIDE: all of them are inside the matrix (else zeros stand for columns past N).
+template <bool INSIDE, int R>
+MOE_DEV void load_rows(const DenseEpi& e, const void* p, int64_t ld, int64_t m, int step, int n, float (&v)[R][8]) {
+  const int end = INSIDE ? n + 8 : e.N;
+  if (e.f32) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = n + i < e.N ? v[i] : 0.f;
-    u[i] = n + i < e.N ? u[i] : 0.f;
-  }
-  if (e.mode == kEpiOut || e.mode == kEpiActBack) {
-    if (e.bias) {
-      float b[8];
-      load8_any(e.bias, e.f32, 0, 0, n, e.N, b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += b[i];
-    }
-    if (e.mode == kEpiOut) {
-      if (e.act != kActNone) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = act_value(e.act, v[i]);
-      }
-      if (e.residual) {
-        float r[8];
-        load8_any(e.residual, e.f32, m, e.ld_residual, n, e.N, r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += r[i];
-      }
-      if (e.f32) store8<false>(static_cast<float*>(e.out) + m * e.ld_out, n, e.N, v);
-      else store8<false>(static_cast<bf16_t*>(e.out) + m * e.ld_out, n, e.N, v);
-    } else {
-      float d[8];
-      load8_any(e.dy, e.f32, m, e.ld_dy, n, e.N, d);  // zeros past N
-#pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] *= act_slope(e.act, v[i]);
-      store_planes(e, e.p0, m, n, d);
-    }
-  } else if (e.mode == kEpiGated) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = act_value(e.act, v[i]) * u[i];
-    store_planes(e, e.p0, m, n, v);
-  } else if (e.mode == kEpiKeep) {
-    store_f32(e.g + m * e.ld_p + n, v);
-    store_f32(e.u + m * e.ld_p + n, u);
+    for (int k = 0; k < R; ++k) load8<INSIDE>(static_cast<const float*>(p) + (m + k * step) * ld, n, end, v[k]);
   } else {
-    float g[8], w[8];
-    load8<true>(e.g + m * e.ld_p + n, 0, 8, g);
-    load8<true>(e.u + m * e.ld_p + n, 0, 8, u);
+    u32x4 raw[R];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = v[i] * u[i] * act_slope(e.act, g[i]);
-    store_planes(e, e.p0, m, n, w);
+    for (int k = 0; k < R; ++k)
+      raw[k] = load8_raw<INSIDE>(static_cast<const bf16_t*>(p) + (m + k * step) * ld, n, end);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float s = act_value(e.act, g[i]);
-      w[i] = v[i] * s;
-      v[i] = s * u[i];
+    for (int k = 0; k < R; ++k) unpack8(raw[k], v[k]);
+  }
+}
+
+// the bias of columns n .. n+7, or zeros
+template <int MODE, bool INSIDE> MOE_DEV void load_bias(const DenseEpi& e, int n, float (&b)[1][8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[0][i] = 0.f;
+  if ((MODE == kEpiOut || MODE == kEpiActBack) && e.bias) load_rows<INSIDE, 1>(e, e.bias, 0, 0, 0, n, b);
+}
+
+// Columns n .. n+7 (n % 8 == 0, n < N) of the R rows m, m + step, ...: their
+// loads are issued together, then the arithmetic, then their stores.
+template <int MODE, bool INSIDE, int R>
+MOE_DEV void dense_epilogue(const DenseEpi& e, int64_t m, int step, int n, float (&v)[R][8], float (&u)[R][8],
+                            const float (&b)[1][8]) {
+  float x[R][8];  // residual, upstream gradient or gate projection
+  if (MODE == kEpiOut && e.residual) load_rows<INSIDE, R>(e, e.residual, e.ld_residual, m, step, n, x);
+  if (MODE == kEpiActBack) load_rows<INSIDE, R>(e, e.dy, e.ld_dy, m, step, n, x);
+  if (MODE == kEpiGatedBack) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int64_t o = (m + k * step) * e.ld_p + n;
+      load8<true>(e.g + o, 0, 8, x[k]);
+      load8<true>(e.u + o, 0, 8, u[k]);
     }
-    store_planes(e, e.p1, m, n, w);
-    store_planes(e, e.p2, m, n, v);
+  }
+  if (!INSIDE) {  // sums of columns past N are of whatever lies there
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[k][i] = n + i < e.N ? v[k][i] : 0.f;
+        u[k][i] = n + i < e.N ? u[k][i] : 0.f;
+      }
+  }
+  if (MODE == kEpiOut || MODE == kEpiActBack) {
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[k][i] += b[0][i];
+  }
+  if (MODE == kEpiOut) {
+    if (e.act != kActNone) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) act_values(e.act, v[k]);
+    }
+    if (e.residual) {
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[k][i] += x[k][i];
+    }
+    const int end = INSIDE ? n + 8 : e.N;
+    if (e.f32) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) store8<INSIDE>(static_cast<float*>(e.out) + (m + k * step) * e.ld_out, n, end, v[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+        store8<INSIDE>(static_cast<bf16_t*>(e.out) + (m + k * step) * e.ld_out, n, end, v[k]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const int64_t o = (m + k * step) * e.ld_p + n;
+    if (MODE == kEpiActBack) {
+      act_slopes(e.act, v[k]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[k][i] *= x[k][i];
+      store_planes(e, e.p0, o, v[k]);
+    } else if (MODE == kEpiGated) {
+      act_values(e.act, v[k]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[k][i] *= u[k][i];
+      store_planes(e, e.p0, o, v[k]);
+    } else if (MODE == kEpiKeep) {
+      store_f32(e.g + o, v[k]);
+      store_f32(e.u + o, u[k]);
+    } else {
+      float s[8], d[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = x[k][i];
+      act_values(e.act, s);
+      act_slopes(e.act, x[k]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        d[i] = v[k][i] * s[i];
+        s[i] *= u[k][i];
+        x[k][i] *= v[k][i] * u[k][i];
+      }
+      store_planes(e, e.p0, o, x[k]);
+      store_planes(e, e.p1, o, d);
+      store_planes(e, e.p2, o, s);
+    }
   }
 }
 
 // ---------------------------------------------------------------- the product
 
-template <int LAYOUT_, bool DUAL_, int TM_, int TN_> struct DenseShape {
-  static constexpr int LAYOUT = LAYOUT_, TM = TM_, TN = TN_;
-  static constexpr bool DUAL = DUAL_;
+template <int LAYOUT_, int MODE_, int TM_, int TN_> struct DenseShape {
+  static constexpr int LAYOUT = LAYOUT_, MODE = MODE_, TM = TM_, TN = TN_;
+  static constexpr bool DUAL = MODE == kEpiGated || MODE == kEpiKeep;
 };
 
 constexpr int kThreads = 256;  // four waves, 2 x 2
@@ -206,6 +257,8 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
   const int s0 = blockIdx.y * g.steps_per_split;
   const int nk = min(g.steps_per_split, all_steps - s0);
 
+  const int64_t lda = g.lda, ldb = g.ldb;
+  const int K = int(g.K);  // entry points bound it far below 2^31
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
@@ -217,11 +270,11 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
 #pragma unroll
   for (int i = 0; i < ACP; ++i) {
     if (A_ROWS) {
-      aoff[i] = uint32_t((8 * (ACP * wave + i) + (lane >> 3)) * g.lda + achunk * 8) * 2u;
+      aoff[i] = uint32_t((8 * (ACP * wave + i) + (lane >> 3)) * lda + achunk * 8) * 2u;
     } else {
       constexpr int KR = 512 / TM, LPR = TM / 8;  // k-rows of a copy, lanes of a k-row
       const int kr = KR * (ACP * wave + i) + lane / LPR;
-      aoff[i] = uint32_t(kr * g.lda + kswz(kr, lane % LPR) * 8) * 2u;
+      aoff[i] = uint32_t(kr * lda + kswz(kr, lane % LPR) * 8) * 2u;
     }
   }
 #pragma unroll
@@ -229,50 +282,74 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
     if (B_ROWS) {
       int r = 8 * (BCP * wave + i) + (lane >> 3);
       if (S::DUAL) r &= TN / 2 - 1;  // waves 0, 1 copy the first matrix's rows, 2, 3 the second's
-      boff[i] = uint32_t(r * g.ldb + achunk * 8) * 2u;
+      boff[i] = uint32_t(r * ldb + achunk * 8) * 2u;
     } else {
       constexpr int KR = 512 / TN, LPR = TN / 8;
       const int kr = KR * (BCP * wave + i) + lane / LPR;
-      boff[i] = uint32_t(kr * g.ldb + kswz(kr, lane % LPR) * 8) * 2u;
+      boff[i] = uint32_t(kr * ldb + kswz(kr, lane % LPR) * 8) * 2u;
     }
   }
-  // rows end at a multiple of 8: a load that a resource ends within reads zeros
-  auto up8 = [](int64_t n) { return (n + 7) & ~int64_t(7); };
-  const int64_t kpad = up8(g.K);
-  // resource over what is left of a matrix of `rows` rows of `cols` from (r, c)
-  auto resource = [](const bf16_t* p, int64_t ld, int64_t rows, int64_t cols, int64_t r, int64_t c) {
-    const int64_t left = ((rows - 1 - r) * ld + cols - c) * 2;
-    return buffer_rsrc(p + r * ld + c, uint32_t(left < 0 ? 0 : left < 0x7ffffff0 ? left : 0x7ffffff0));
+  // Sources of the next step to be copied.  A resource starts at the step's
+  // first element; `end` is what it spans, counted from the segment's first
+  // step (k-contiguous: to the end of the tile's last row, rows ending at a
+  // multiple of 8) or from its own (k-slow: the k-rows that are left).
+  const int kpad = (K + 7) & ~7;
+  const int64_t cols_a = ((g.M + 7) & ~int64_t(7)) - m0, cols_b = ((int64_t(g.N) + 7) & ~int64_t(7)) - n0;
+  const int rows_a = int(std::min<int64_t>(TM, g.M - m0)), rows_b = min(S::DUAL ? TN / 2 : TN, g.N - n0);
+  const uint32_t end_a = A_ROWS ? uint32_t(((rows_a - 1) * lda + kpad) * 2) : uint32_t((63 * lda + cols_a) * 2);
+  const uint32_t end_b = B_ROWS ? uint32_t(((rows_b - 1) * ldb + kpad) * 2) : uint32_t((63 * ldb + cols_b) * 2);
+  const int64_t step_a = (A_ROWS ? BK : BK * lda) * 2, step_b = (B_ROWS ? BK : BK * ldb) * 2;
+  int seg = s0 / per_segment, kk = (s0 - seg * per_segment) * BK, left = nk;
+  const char *pa, *pb;
+  uint32_t span_a, span_b;
+  auto spans = [&]() __attribute__((always_inline)) {
+    const int krows = min(BK, K - kk);
+    span_a = A_ROWS ? end_a - uint32_t(kk) * 2u : end_a - uint32_t((BK - krows) * lda * 2);
+    span_b = B_ROWS ? end_b - uint32_t(kk) * 2u : end_b - uint32_t((BK - krows) * ldb * 2);
   };
-  int seg = s0 / per_segment, kk = (s0 - seg * per_segment) * BK;  // of the next step to be copied
-  auto copy_a = [&](int i, __amdgpu_buffer_rsrc_t rs, uint32_t beyond, int stage) {
-    copy_to_lds_async16(rs, A_ROWS ? aoff[i] | beyond : aoff[i], As + stage * ASTAGE + (ACP * wave + i) * 512);
+  // (the segments' pointers are read where the arguments lie: indexing the
+  // by-value copy makes this compiler keep one on the stack)
+  typedef const __attribute__((address_space(4))) DenseArgs* KernelArgs;
+  const KernelArgs table = (KernelArgs)__builtin_amdgcn_kernarg_segment_ptr();
+  auto seek = [&]() __attribute__((always_inline)) {
+    const int64_t k = kk;
+    const bf16_t* qb = S::DUAL && wave >= 2 ? table->b2[seg] : table->b[seg];
+    pa = reinterpret_cast<const char*>(table->a[seg] + (A_ROWS ? m0 * lda + k : k * lda + m0));
+    pb = reinterpret_cast<const char*>(qb + (B_ROWS ? n0 * ldb + k : k * ldb + n0));
+    spans();
   };
-  auto copy_b = [&](int i, __amdgpu_buffer_rsrc_t rs, uint32_t beyond, int stage) {
-    copy_to_lds_async16(rs, B_ROWS ? boff[i] | beyond : boff[i], Bs + stage * BSTAGE + (BCP * wave + i) * 512);
-  };
+  seek();
   struct Step {
     __amdgpu_buffer_rsrc_t a, b;
     uint32_t beyond;
   };
-  // sources of the next step; the position then moves on (past the last step
-  // it stays, and the last step is copied again: every step has its copies)
-  int left = nk;
-  auto next_step = [&]() {
-    const bf16_t* pa = g.a[seg];
-    const bf16_t* pb = S::DUAL && wave >= 2 ? g.b2[seg] : g.b[seg];
+  auto this_step = [&]() {
     Step s;
-    s.a = A_ROWS ? resource(pa, g.lda, g.M, kpad, m0, kk) : resource(pa, g.lda, g.K, up8(g.M), kk, m0);
-    s.b = B_ROWS ? resource(pb, g.ldb, g.N, kpad, n0, kk) : resource(pb, g.ldb, g.K, up8(g.N), kk, n0);
+    s.a = buffer_rsrc(pa, span_a);
+    s.b = buffer_rsrc(pb, span_b);
     s.beyond = kk + achunk * 8 >= kpad ? kBeyond : 0u;
-    if (--left > 0) {
-      kk += BK;
-      if (kk >= g.K) {
-        kk = 0;
-        ++seg;
-      }
-    }
     return s;
+  };
+  // (past the last step the position stays, and the last step is copied again:
+  // every step has its copies)
+  auto advance = [&]() __attribute__((always_inline)) {
+    if (--left <= 0) return;
+    kk += BK;
+    if (kk >= K) {
+      kk = 0;
+      ++seg;
+      seek();
+    } else {
+      pa += step_a;
+      pb += step_b;
+      spans();
+    }
+  };
+  auto copy_a = [&](int i, const Step& s, int stage) {
+    copy_to_lds_async16(s.a, A_ROWS ? aoff[i] | s.beyond : aoff[i], As + stage * ASTAGE + (ACP * wave + i) * 512);
+  };
+  auto copy_b = [&](int i, const Step& s, int stage) {
+    copy_to_lds_async16(s.b, B_ROWS ? boff[i] | s.beyond : boff[i], Bs + stage * BSTAGE + (BCP * wave + i) * 512);
   };
 
   f32x16 acc[MB][NB];
@@ -307,7 +384,7 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
 #pragma unroll
     for (int q = 0; q < MB * NB; ++q) {
       const int i = q / NB, j = q % NB;
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
       constexpr int PER = (MB + NB + MB * NB - 1) / (MB * NB);
 #pragma unroll
       for (int r = 0; r < PER; ++r)
@@ -318,27 +395,23 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
   };
   auto none = [](int) {};
 
-  {
-    const Step s = next_step();
 #pragma unroll
-    for (int i = 0; i < ACP; ++i) copy_a(i, s.a, s.beyond, 0);
+  for (int st = 0; st < 2; ++st) {
+    const Step s = this_step();
 #pragma unroll
-    for (int i = 0; i < BCP; ++i) copy_b(i, s.b, s.beyond, 0);
+    for (int i = 0; i < ACP; ++i) copy_a(i, s, st);
+#pragma unroll
+    for (int i = 0; i < BCP; ++i) copy_b(i, s, st);
+    advance();
   }
-  __builtin_amdgcn_s_waitcnt(kWaitCopies);
+  __builtin_amdgcn_s_waitcnt(wait_copies(ACP + BCP));  // the first step's
   __builtin_amdgcn_s_barrier();
-  {
-    const Step s = next_step();
-#pragma unroll
-    for (int i = 0; i < ACP; ++i) copy_a(i, s.a, s.beyond, 1);
-#pragma unroll
-    for (int i = 0; i < BCP; ++i) copy_b(i, s.b, s.beyond, 1);
-  }
   Frags f0, f1;
 #pragma unroll
   for (int q = 0; q < MB + NB; ++q) read(f0, q, 0, 0);
   for (int kt = 0; kt < nk; ++kt) {
     const int st = kt & 1;
+    const Step next = this_step();
     slice(f0, f1, st, 1, none);
     slice(f1, f0, st, 2, none);
     slice(f0, f1, st, 3, none);
@@ -346,30 +419,61 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
     // one are done; behind the barrier everyone's
     __builtin_amdgcn_s_waitcnt(kWaitAll);
     __builtin_amdgcn_s_barrier();
-    const Step s = next_step();
     constexpr int PER = (ACP + BCP + MB * NB - 1) / (MB * NB);
     slice(f1, f0, st ^ 1, 0, [&](int q) {
 #pragma unroll
       for (int r = 0; r < PER; ++r) {
         const int c = q * PER + r;
-        if (c < ACP) copy_a(c, s.a, s.beyond, st);
-        else if (c < ACP + BCP) copy_b(c - ACP, s.b, s.beyond, st);
+        if (c < ACP) copy_a(c, next, st);
+        else if (c < ACP + BCP) copy_b(c - ACP, next, st);
       }
     });
+    advance();
   }
   __builtin_amdgcn_s_waitcnt(kWaitAll);  // no copy left in flight
   __syncthreads();
 
-  // ---- epilogue.  Accumulator v of lane l: row 8 (v/4) + 4 (l/32) + v%4,
-  // column l%32.  Each wave passes 32 rows of its columns at a time through
-  // LDS (float32), so that a lane has 8 consecutive columns of a row.
+  // ---- epilogue.  B is the MFMA's first operand, so accumulator v of lane l
+  // is row l%32, column 8 (v/4) + 4 (l/32) + v%4: four columns in a row.  Each
+  // wave passes 32 rows of its columns at a time through LDS (float32), so that
+  // a lane has 8 consecutive columns of a row.
   constexpr int WC = 32 * NB;             // staged columns of a wave
   constexpr int OC = S::DUAL ? WC / 2 : WC;  // output columns of a wave
   constexpr int PITCH = WC * 4 + 16;      // bytes
   static_assert(4 * 32 * PITCH <= 2 * (ASTAGE + BSTAGE) * 2, "the staging rows fit the stages");
   constexpr int LPR = OC / 8, RPI = 64 / LPR;  // lanes of a row, rows at a time
   lds_u8* slot = (lds_u8*)smem + wave * 32 * PITCH;
-  const int nw = n0 + wn * OC;
+  const int c = 8 * (lane % LPR), n = n0 + wn * OC + c;
+  float bias[1][8];
+  if (g.split == 1) load_bias<S::MODE, false>(g.epi, n, bias);
+  // R rows of this lane from row r of the staged 32, which are rows mrow ...
+  auto finish = [&](int64_t mrow, int r, auto inside, auto rows) __attribute__((always_inline)) {
+    constexpr int R = decltype(rows)::value;
+    float v[R][8], u[R][8];
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const lds_u8* at = slot + (r + k * RPI) * PITCH + 4 * c + 16 * h;
+        const f32x4 p = *(const lds_f32x4*)at;
+        f32x4 q = {0.f, 0.f, 0.f, 0.f};
+        if (S::DUAL) q = *(const lds_f32x4*)(at + 4 * OC);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { v[k][4 * h + i] = p[i]; u[k][4 * h + i] = q[i]; }
+      }
+    if (g.split == 1) {
+      dense_epilogue<S::MODE, decltype(inside)::value, R>(g.epi, mrow + r, RPI, n, v, u, bias);
+    } else {
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        float* p = g.part + (int64_t(blockIdx.y) * (S::DUAL ? 2 : 1) * g.M + mrow + r + k * RPI) * g.ld_part + n;
+        store_f32(p, v[k]);
+        if (S::DUAL) store_f32(p + g.M * g.ld_part, u[k]);
+      }
+    }
+  };
+  constexpr int AHEAD = 32 / RPI < 4 ? 32 / RPI : 4;  // rows at a time where all are inside
+  const bool whole = m0 + TM <= g.M && n0 + NCOL <= g.N;
 #pragma unroll 1
   for (int blk = 0; blk < MB; ++blk) {
     const int64_t mrow = m0 + wm * (TM / 2) + 32 * blk;
@@ -380,63 +484,53 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
 #pragma unroll
       for (int j = 0; j < NB; ++j)
 #pragma unroll
-        for (int v = 0; v < 16; ++v)
-          *(lds_f32*)(slot + (8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)) * PITCH + 4 * (32 * j + (lane & 31))) =
-              acc[i][j][v];
+        for (int v = 0; v < 16; v += 4)
+          *(lds_f32x4*)(slot + (lane & 31) * PITCH + 4 * (32 * j + 2 * v + 4 * (lane >> 5))) =
+              f32x4{acc[i][j][v], acc[i][j][v + 1], acc[i][j][v + 2], acc[i][j][v + 3]};
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    const int c = 8 * (lane % LPR), n = nw + c;
+    if (whole) {
 #pragma unroll 1
-    for (int r = lane / LPR; r < 32; r += RPI) {
-      const int64_t m = mrow + r;
-      if (m >= g.M || n >= g.N) continue;
-      float v[8], u[8];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const f32x4 x = *(const lds_f32x4*)(slot + r * PITCH + 4 * c + 16 * h);
-        f32x4 y = {0.f, 0.f, 0.f, 0.f};
-        if (S::DUAL) y = *(const lds_f32x4*)(slot + r * PITCH + 4 * (OC + c) + 16 * h);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) { v[4 * h + k] = x[k]; u[4 * h + k] = y[k]; }
-      }
-      if (g.split > 1) {
-        float* p = g.part + (int64_t(blockIdx.y) * (S::DUAL ? 2 : 1) * g.M + m) * g.ld_part + n;
-        store_f32(p, v);
-        if (S::DUAL) store_f32(p + g.M * g.ld_part, u);
-      } else {
-        dense_epilogue(g.epi, m, n, v, u);
-      }
+      for (int r = lane / LPR; r < 32; r += RPI * AHEAD)
+        finish(mrow, r, std::true_type{}, std::integral_constant<int, AHEAD>{});
+    } else {
+#pragma unroll 1
+      for (int r = lane / LPR; r < 32; r += RPI)
+        if (mrow + r < g.M && n < g.N) finish(mrow, r, std::false_type{}, std::integral_constant<int, 1>{});
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 }
 
 // sums of a split contraction, in split order, and the epilogue on them
-__global__ __launch_bounds__(256) void dense_join_kernel(DenseArgs g) {
+template <int MODE> __global__ __launch_bounds__(256) void dense_join_kernel(DenseArgs g) {
+  constexpr bool DUAL = MODE == kEpiGated || MODE == kEpiKeep;
   const int nc = (g.N + 7) / 8;
   const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
   const int64_t m = id / nc;
   if (m >= g.M) return;
   const int n = int(id - m * nc) * 8;
-  float v[8], u[8];
+  float v[1][8], u[1][8], b[1][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.f;
+  for (int i = 0; i < 8; ++i) v[0][i] = u[0][i] = 0.f;
+  load_bias<MODE, false>(g.epi, n, b);
   const float* p = g.part + m * g.ld_part + n;
   const int64_t step = g.M * g.ld_part;
+#pragma unroll 4
   for (int s = 0; s < g.split; ++s) {
     float x[8];
     load8<true>(p, 0, 8, x);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += x[i];
+    for (int i = 0; i < 8; ++i) v[0][i] += x[i];
     p += step;
-    if (g.dual) {
+    if (DUAL) {
       load8<true>(p, 0, 8, x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] += x[i];
+      for (int i = 0; i < 8; ++i) u[0][i] += x[i];
       p += step;
     }
   }
-  dense_epilogue(g.epi, m, n, v, u);
+  dense_epilogue<MODE, false, 1>(g.epi, m, 0, n, v, u, b);
 }
 
 // ---------------------------------------------------------------- operands
@@ -453,9 +547,8 @@ __global__ __launch_bounds__(256) void dense_pack_kernel(const TE* src, int64_t 
   load8<false>(src + r * ld_src, c, cols, v);
   DenseEpi e{};
   e.f32 = sizeof(TE) == 4;
-  e.ld_p = ld_dst;
   e.plane = rows * ld_dst;
-  store_planes(e, dst, r, c, v);
+  store_planes(e, dst, r * ld_dst + c, v);
 }
 
 // Column sums.  A workgroup takes 256 columns, 8 a thread, and a range of rows
@@ -541,9 +634,13 @@ template <class S> hipError_t launch_shape(const DenseArgs& g, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int LAYOUT, bool DUAL> hipError_t launch_layout(const DenseArgs& g, const DensePlan& p, hipStream_t st) {
-  if (p.tm == 256) return launch_shape<DenseShape<LAYOUT, DUAL, 256, 256>>(g, st);
-  return launch_shape<DenseShape<LAYOUT, DUAL, 128, 128>>(g, st);
+template <int LAYOUT, int MODE> hipError_t launch_mode(const DenseArgs& g, const DensePlan& p, hipStream_t st) {
+  const hipError_t err = p.tm == 256 ? launch_shape<DenseShape<LAYOUT, MODE, 256, 256>>(g, st)
+                                     : launch_shape<DenseShape<LAYOUT, MODE, 128, 128>>(g, st);
+  if (err != hipSuccess || g.split == 1) return err;
+  const int64_t threads = g.M * ((g.N + 7) / 8);
+  hipLaunchKernelGGL((dense_join_kernel<MODE>), dim3(unsigned((threads + 255) / 256)), dim3(256), 0, st, g);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -557,20 +654,21 @@ size_t dense_part_bytes(int layout, int64_t M, int N, int64_t K, int segments, i
 hipError_t launch_dense(const DenseArgs& args, int layout, hipStream_t st) {
   DenseArgs g = args;
   if (g.M <= 0 || g.N <= 0) return hipSuccess;
-  if (g.segments < 1 || g.segments > kMaxSegments || (g.dual && layout != kNT)) return hipErrorInvalidValue;
+  if (g.segments < 1 || g.segments > kMaxSegments || g.dual != (g.epi.mode == kEpiGated || g.epi.mode == kEpiKeep)) return hipErrorInvalidValue;
   const DensePlan p = dense_plan(layout, g.M, g.N, g.K, g.segments, g.dual);
   g.split = p.split;
   g.steps_per_split = p.steps;
   g.ld_part = (int64_t(g.N) + 7) & ~int64_t(7);
   if (g.split > 1 && g.part == nullptr) return hipErrorInvalidValue;
-  hipError_t err;
-  if (layout == kNT) err = g.dual ? launch_layout<kNT, true>(g, p, st) : launch_layout<kNT, false>(g, p, st);
-  else if (layout == kNN) err = launch_layout<kNN, false>(g, p, st);
-  else err = launch_layout<kTN, false>(g, p, st);
-  if (err != hipSuccess || g.split == 1) return err;
-  const int64_t threads = g.M * ((g.N + 7) / 8);
-  hipLaunchKernelGGL(dense_join_kernel, dim3(unsigned((threads + 255) / 256)), dim3(256), 0, st, g);
-  return hipGetLastError();
+  // the products that the operators are made of
+  if (layout == kNT && g.epi.mode == kEpiOut) return launch_mode<kNT, kEpiOut>(g, p, st);
+  if (layout == kNT && g.epi.mode == kEpiGated) return launch_mode<kNT, kEpiGated>(g, p, st);
+  if (layout == kNT && g.epi.mode == kEpiKeep) return launch_mode<kNT, kEpiKeep>(g, p, st);
+  if (layout == kNT && g.epi.mode == kEpiActBack) return launch_mode<kNT, kEpiActBack>(g, p, st);
+  if (layout == kNN && g.epi.mode == kEpiOut) return launch_mode<kNN, kEpiOut>(g, p, st);
+  if (layout == kNN && g.epi.mode == kEpiGatedBack) return launch_mode<kNN, kEpiGatedBack>(g, p, st);
+  if (layout == kTN && g.epi.mode == kEpiOut) return launch_mode<kTN, kEpiOut>(g, p, st);
+  return hipErrorInvalidValue;
 }
 
 hipError_t launch_dense_pack(const void* src, int64_t ld_src, bool f32, int64_t rows, int cols, bf16_t* dst,
