@@ -433,35 +433,56 @@ def bias_update(cfg: _Cfg, T: int, counts: torch.Tensor, bias: torch.Tensor, gam
 # ---------------------------------------------------------------- around the expert layer
 
 
+# These run for every tensor of every call, beside kernels of a few microseconds: one pass over the
+# properties that are right in an ordinary call, and the reason only where one is not.
+
+
+def _refuse(t: torch.Tensor, name: str, dtype, shape):
+    """Raises with what is wrong with a tensor."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.stride(-1) != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    raise ValueError(f"{name} must be contiguous")
+
+
 def _rows(t: Optional[torch.Tensor], name: str, dtype, T: int, cols: int):
     """(pointer, row stride) of [T][cols] activations: contiguous rows, any stride between them."""
     if t is None:
         return None, 0
-    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != cols:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, cols)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != (T, cols) or t.dtype != dtype or not t.is_cuda:
+        _refuse(t, name, dtype, (T, cols))
     ld, step = t.stride()
     if step != 1 and cols > 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
+        _refuse(t, name, dtype, (T, cols))
     # the stride of a dimension of one is arbitrary
-    return t.data_ptr(), ld if T > 1 else max(cols, 1)
+    return t.data_ptr(), ld if T > 1 else cols
 
 
 def _packed(t: Optional[torch.Tensor], name: str, dtype, *shape):
     """Pointer to a packed tensor of this shape, or None."""
     if t is None:
         return None
-    _check(t, name, dtype, shape)
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        _refuse(t, name, dtype, shape)
     return t.data_ptr()
 
 
-def _need(**tensors):
-    for name, t in tensors.items():
-        if t is None:
-            raise ValueError(f"{name} is required")
+def _queue(stream) -> int:
+    """The stream's handle; None is the current one, asked for without making a Stream object."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _need(t: Optional[torch.Tensor], name: str) -> torch.Tensor:
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return t
 
 
 def _ws(ws: Optional[torch.Tensor]):
@@ -506,12 +527,11 @@ def norm_forward(cfg: _NormCfg, residual: torch.Tensor, branch: Optional[torch.T
 
     ``params``: w_post, b_post, w_pre, b_pre ([hidden]) and gate ([T / gate_rows][hidden]); absent
     or None ones as in ``include/moe.h``.  ``u`` or ``h`` may be None."""
-    _need(residual=residual)
-    T, H, dt = residual.shape[0], cfg.hidden, _TORCH_DT[cfg.dtype]
+    T, H, dt = _need(residual, "residual").shape[0], cfg.hidden, _TORCH_DT[cfg.dtype]
     p = _norm_params(cfg, T, dt, params)
     _call("moe_norm_forward", cfg, T, *_rows(residual, "residual", dt, T, H),
           *_rows(branch, "branch", dt, T, H), p, *_rows(u, "u", dt, T, H), *_rows(h, "h", dt, T, H),
-          _stream(stream))
+          _queue(stream))
 
 
 def norm_backward_workspace_bytes(cfg: _NormCfg, T: int) -> int:
@@ -528,8 +548,7 @@ def norm_backward(cfg: _NormCfg, residual: torch.Tensor, branch: Optional[torch.
                   stream=None) -> None:
     """moe_norm_backward: gradients of <du, u> + <dh, h> into the tensors of ``grads``
     (residual, branch, w_post, b_post, w_pre, b_pre, gate; those absent are not formed)."""
-    _need(residual=residual)
-    T, H, n, dt = residual.shape[0], cfg.hidden, cfg.gate_rows, _TORCH_DT[cfg.dtype]
+    T, H, n, dt = _need(residual, "residual").shape[0], cfg.hidden, cfg.gate_rows, _TORCH_DT[cfg.dtype]
     p = _norm_params(cfg, T, dt, params)
     vec = [_packed(grads.get(k), f"grads[{k}]", dt, H) for k in ("w_post", "b_post", "w_pre", "b_pre")]
     g = _NormGrads(*_rows(grads.get("residual"), "grads[residual]", dt, T, H),
@@ -537,7 +556,7 @@ def norm_backward(cfg: _NormCfg, residual: torch.Tensor, branch: Optional[torch.
                    _packed(grads.get("gate"), "grads[gate]", dt, T // n if n > 0 else 0, H))
     _call("moe_norm_backward", cfg, T, *_rows(residual, "residual", dt, T, H),
           *_rows(branch, "branch", dt, T, H), p, *_rows(du, "du", dt, T, H),
-          *_rows(dh, "dh", dt, T, H), g, *_ws(ws), _stream(stream))
+          *_rows(dh, "dh", dt, T, H), g, *_ws(ws), _queue(stream))
 
 
 def make_linear_cfg(in_dim: int, out_dim: int, act: str = "none", dtype=BF16) -> _LinearCfg:
@@ -565,11 +584,10 @@ def linear_forward(cfg: _LinearCfg, x: torch.Tensor, w: torch.Tensor, y: torch.T
                    ws: torch.Tensor, bias: Optional[torch.Tensor] = None,
                    residual: Optional[torch.Tensor] = None, stream=None) -> None:
     """moe_linear_forward: y = residual + act(x w^T + bias)."""
-    _need(x=x, w=w, y=y)
-    T, K, N, dt = x.shape[0], cfg.in_dim, cfg.out_dim, _TORCH_DT[cfg.dtype]
-    _call("moe_linear_forward", cfg, T, *_rows(x, "x", dt, T, K), _packed(w, "w", dt, N, K),
+    T, K, N, dt = _need(x, "x").shape[0], cfg.in_dim, cfg.out_dim, _TORCH_DT[cfg.dtype]
+    _call("moe_linear_forward", cfg, T, *_rows(x, "x", dt, T, K), _packed(_need(w, "w"), "w", dt, N, K),
           _packed(bias, "bias", dt, N), *_rows(residual, "residual", dt, T, N),
-          *_rows(y, "y", dt, T, N), *_ws(ws), _stream(stream))
+          *_rows(_need(y, "y"), "y", dt, T, N), *_ws(ws), _queue(stream))
 
 
 def linear_backward(cfg: _LinearCfg, x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor,
@@ -577,11 +595,10 @@ def linear_backward(cfg: _LinearCfg, x: torch.Tensor, w: torch.Tensor, dy: torch
                     dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
                     dbias: Optional[torch.Tensor] = None, stream=None) -> None:
     """moe_linear_backward: gradients of <dy, y> into those of dx, dw and dbias that are given."""
-    _need(x=x, w=w, dy=dy)
-    T, K, N, dt = x.shape[0], cfg.in_dim, cfg.out_dim, _TORCH_DT[cfg.dtype]
-    _call("moe_linear_backward", cfg, T, *_rows(x, "x", dt, T, K), _packed(w, "w", dt, N, K),
-          _packed(bias, "bias", dt, N), *_rows(dy, "dy", dt, T, N), *_rows(dx, "dx", dt, T, K),
-          _packed(dw, "dw", dt, N, K), _packed(dbias, "dbias", dt, N), *_ws(ws), _stream(stream))
+    T, K, N, dt = _need(x, "x").shape[0], cfg.in_dim, cfg.out_dim, _TORCH_DT[cfg.dtype]
+    _call("moe_linear_backward", cfg, T, *_rows(x, "x", dt, T, K), _packed(_need(w, "w"), "w", dt, N, K),
+          _packed(bias, "bias", dt, N), *_rows(_need(dy, "dy"), "dy", dt, T, N), *_rows(dx, "dx", dt, T, K),
+          _packed(dw, "dw", dt, N, K), _packed(dbias, "dbias", dt, N), *_ws(ws), _queue(stream))
 
 
 def make_ffn_cfg(hidden: int, inter: int, act: str = "silu", dtype=BF16) -> _FfnCfg:
@@ -607,28 +624,27 @@ def alloc_ffn_backward_workspace(cfg: _FfnCfg, T: int, device="cuda") -> torch.T
 
 def _ffn_weights(cfg: _FfnCfg, dt, w: Dict[str, torch.Tensor]):
     H, I = cfg.hidden, cfg.inter
-    _need(**{k: w.get(k) for k in ("w_gate", "w_up", "w_down")})
-    return (_packed(w["w_gate"], "w_gate", dt, I, H), _packed(w["w_up"], "w_up", dt, I, H),
-            _packed(w["w_down"], "w_down", dt, H, I))
+    return (_packed(_need(w.get("w_gate"), "w_gate"), "w_gate", dt, I, H),
+            _packed(_need(w.get("w_up"), "w_up"), "w_up", dt, I, H),
+            _packed(_need(w.get("w_down"), "w_down"), "w_down", dt, H, I))
 
 
 def ffn_forward(cfg: _FfnCfg, x: torch.Tensor, weights: Dict[str, torch.Tensor], y: torch.Tensor,
                 ws: torch.Tensor, residual: Optional[torch.Tensor] = None, stream=None) -> None:
     """moe_ffn_forward: y = residual + (act(x w_gate^T) * (x w_up^T)) w_down^T."""
-    _need(x=x, y=y)
-    T, H, dt = x.shape[0], cfg.hidden, _TORCH_DT[cfg.dtype]
+    T, H, dt = _need(x, "x").shape[0], cfg.hidden, _TORCH_DT[cfg.dtype]
     _call("moe_ffn_forward", cfg, T, *_rows(x, "x", dt, T, H), *_ffn_weights(cfg, dt, weights),
-          *_rows(residual, "residual", dt, T, H), *_rows(y, "y", dt, T, H), *_ws(ws),
-          _stream(stream))
+          *_rows(residual, "residual", dt, T, H), *_rows(_need(y, "y"), "y", dt, T, H), *_ws(ws),
+          _queue(stream))
 
 
 def ffn_backward(cfg: _FfnCfg, x: torch.Tensor, weights: Dict[str, torch.Tensor],
                  dy: torch.Tensor, dx: torch.Tensor, dw_gate: torch.Tensor, dw_up: torch.Tensor,
                  dw_down: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """moe_ffn_backward: gradients of <dy, y> into dx and the weight gradients."""
-    _need(x=x, dy=dy, dx=dx, dw_gate=dw_gate, dw_up=dw_up, dw_down=dw_down)
-    T, H, I, dt = x.shape[0], cfg.hidden, cfg.inter, _TORCH_DT[cfg.dtype]
+    T, H, I, dt = _need(x, "x").shape[0], cfg.hidden, cfg.inter, _TORCH_DT[cfg.dtype]
     _call("moe_ffn_backward", cfg, T, *_rows(x, "x", dt, T, H), *_ffn_weights(cfg, dt, weights),
-          *_rows(dy, "dy", dt, T, H), *_rows(dx, "dx", dt, T, H),
-          _packed(dw_gate, "dw_gate", dt, I, H), _packed(dw_up, "dw_up", dt, I, H),
-          _packed(dw_down, "dw_down", dt, H, I), *_ws(ws), _stream(stream))
+          *_rows(_need(dy, "dy"), "dy", dt, T, H), *_rows(_need(dx, "dx"), "dx", dt, T, H),
+          _packed(_need(dw_gate, "dw_gate"), "dw_gate", dt, I, H),
+          _packed(_need(dw_up, "dw_up"), "dw_up", dt, I, H),
+          _packed(_need(dw_down, "dw_down"), "dw_down", dt, H, I), *_ws(ws), _queue(stream))

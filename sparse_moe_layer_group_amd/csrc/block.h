@@ -36,6 +36,36 @@ MOE_DEV void act_values(int act, float (&v)[8]) {
   else if (act == kActGelu) each8(v, gelu_value);
   else if (act == kActRelu) each8(v, relu_value);
 }
+// v becomes the activation, d its slope
+MOE_DEV void act_both(int act, float (&v)[8], float (&d)[8]) {
+  if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float s = sigmoidf(v[i]);
+      d[i] = s * (1.0f + v[i] * (1.0f - s));
+      v[i] *= s;
+    }
+  } else if (act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float z = v[i], phi = 0.5f * erfcf(-0.70710678118654752f * z);
+      d[i] = phi + z * 0.39894228040143268f * expf(-0.5f * z * z);
+      v[i] = z * phi;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      d[i] = act == kActRelu ? relu_slope(v[i]) : 1.f;
+      v[i] = act == kActRelu ? relu_value(v[i]) : v[i];
+    }
+  }
+}
+MOE_DEV float act_one(int act, float z) {
+  return act == kActSilu ? siluf(z) : act == kActGelu ? gelu_value(z) : act == kActRelu ? relu_value(z) : z;
+}
+MOE_DEV float slope_one(int act, float z) {
+  return act == kActSilu ? silu_slope(z) : act == kActGelu ? gelu_slope(z) : act == kActRelu ? relu_slope(z) : 1.f;
+}
 MOE_DEV void act_slopes(int act, float (&v)[8]) {
   if (act == kActSilu) each8(v, silu_slope);
   else if (act == kActGelu) each8(v, gelu_slope);
@@ -191,17 +221,44 @@ struct DenseArgs {
   int64_t M, K;                    // K of one segment
   int N, segments, dual;
   int split, steps_per_split;      // set by the launcher
-  float* part;                     // split > 1: [split][1 + dual][M][ld_part]
+  float* part;                     // (set by the launcher) split > 1: [split][1 + dual][M][ld_part]
   int64_t ld_part;
   DenseEpi epi;
 };
-size_t dense_part_bytes(int layout, int64_t M, int N, int64_t K, int segments, int dual);
-hipError_t launch_dense(const DenseArgs& a, int layout, hipStream_t st);
+// Up to three products of one layout, mode, contraction and M N go in one
+// launch (the gate, up and down matrices' gradients).
+constexpr int kMaxGroup = 3;
+struct DenseGroup { DenseArgs g[kMaxGroup]; };
+size_t dense_part_bytes(int64_t M, int N, int64_t K, int segments, int dual, int count);
+hipError_t launch_dense(const DenseGroup& group, int count, int layout, float* part, hipStream_t st);
 
-// planes of an operand: dst [f32 ? 3 : 1][rows][ld_dst] with zeros past cols.
-// float32 values are split exactly into three bfloat16 parts.
-hipError_t launch_dense_pack(const void* src, int64_t ld_src, bool f32, int64_t rows, int cols, bf16_t* dst,
-                             int64_t ld_dst, hipStream_t st);
+// ---------------------------------------------------------------- few tokens (dense_stream.hip)
+
+// out[t][n] = residual + act(x w^T + bias), or with w2: act(x w^T) * (x w2^T),
+// all of one type; w and w2 are packed [N][K]
+struct DenseStreamArgs {
+  const void *x, *w, *w2, *bias, *residual;
+  void* out;
+  int64_t ld_x, ld_residual, ld_out;
+  int T, N, K, act;
+};
+constexpr int kStreamTokens = 64;
+hipError_t launch_dense_stream(const DenseStreamArgs& a, bool f32, hipStream_t st);
+
+// ---------------------------------------------------------------- operands
+
+// Planes of operands, all in one launch: dst [f32 ? 3 : 1][rows][ld_dst] with
+// zeros past cols.  float32 values are split exactly into three bfloat16 parts.
+struct PackJob {
+  const void* src;
+  int64_t ld_src, rows;
+  int cols;
+  bf16_t* dst;
+  int64_t ld_dst;
+};
+constexpr int kMaxPacks = 5;
+struct PackJobs { PackJob j[kMaxPacks]; };
+hipError_t launch_dense_pack(const PackJobs& jobs, int count, bool f32, hipStream_t st);
 
 // out[n] = sum over rows of src[r][n]; planes as above (n_planes 1 or 3) or, n_planes 0, float32
 size_t dense_colsum_bytes(int64_t rows, int cols);

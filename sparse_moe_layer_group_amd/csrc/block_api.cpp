@@ -143,15 +143,24 @@ Source source(Carver& w, bool f32, const void* p, int64_t ld, int64_t rows, int 
 bool direct(const Source& s) {
   return s.cols % 8 == 0 && s.ld % 8 == 0 && (reinterpret_cast<uintptr_t>(s.p) & 15) == 0;
 }
-hipError_t operand(const Source& s, bool f32, Mat& m, bool as_is, hipStream_t st) {
-  if (!f32 && as_is) {
-    const bf16_t* p = static_cast<const bf16_t*>(s.p);
-    m = Mat{{p, p, p}, s.ld};
-    return hipSuccess;
+// The operands of a call; what has to be laid out anew is, in one launch.
+struct Operands {
+  bool f32;
+  moe::PackJobs jobs;
+  int count = 0;
+  explicit Operands(bool f) : f32(f) {}
+  Mat add(const Source& s, bool as_is) {
+    if (!f32 && as_is) {
+      const bf16_t* p = static_cast<const bf16_t*>(s.p);
+      return Mat{{p, p, p}, s.ld};
+    }
+    const Mat m = planes_at(f32, s.room, s.rows, s.cols);
+    jobs.j[count++] = moe::PackJob{s.p, s.ld, s.rows, s.cols, s.room, m.ld};
+    return m;
   }
-  m = planes_at(f32, s.room, s.rows, s.cols);
-  return moe::launch_dense_pack(s.p, s.ld, f32, s.rows, s.cols, s.room, m.ld, st);
-}
+  Mat add(const Source& s) { return add(s, direct(s)); }
+  hipError_t lay_out(hipStream_t st) const { return moe::launch_dense_pack(jobs, count, f32, st); }
+};
 
 // Segments of A B over the planes, smallest terms first.  Of float32's nine
 // pairs, mid lo, lo mid and lo lo are below 2^-24 of the product and left out.
@@ -171,12 +180,11 @@ void add_segments(moe::DenseArgs& g, bool f32, const Mat& A, const Mat& B, const
     g.b2[s] = B2 != nullptr ? B2->p[b] : nullptr;
   }
 }
-moe::DenseArgs product(int64_t M, int N, int64_t K, float* part, int mode, bool f32) {
+moe::DenseArgs product(int64_t M, int N, int64_t K, int mode, bool f32) {
   moe::DenseArgs g{};
   g.M = M;
   g.N = N;
   g.K = K;
-  g.part = part;
   g.epi.mode = mode;
   g.epi.f32 = f32;
   g.epi.M = M;
@@ -188,9 +196,20 @@ void stage_to(moe::DenseEpi& e, const Mat& m, int64_t rows) {
   e.ld_p = m.ld;
   e.plane = rows * m.ld;
 }
-size_t part_bytes(int layout, int64_t M, int N, int64_t K, bool f32, int pairs = 1, int dual = 0) {
-  return moe::dense_part_bytes(layout, M, N, K, pairs * (f32 ? kPairs : 1), dual);
+size_t part_bytes(int64_t M, int N, int64_t K, bool f32, int pairs = 1, int dual = 0, int count = 1) {
+  return moe::dense_part_bytes(M, N, K, pairs * (f32 ? kPairs : 1), dual, count);
 }
+hipError_t launch(const moe::DenseArgs& g, int layout, float* part, hipStream_t st) {
+  moe::DenseGroup group{};
+  group.g[0] = g;
+  return moe::launch_dense(group, 1, layout, part, st);
+}
+
+// Whether a forward product goes to the weight-streaming kernel.  bfloat16: up
+// to 16 tokens (one MFMA's; at hidden 7168 and inter 2048 a block of 16 takes
+// 25 us against 33 us by tiles, of 32 39 against 34).  float32: to 64, as the
+// tiles need the weights laid out as three planes first (130 against 182 us).
+bool streams(int64_t T, bool f32) { return T <= (f32 ? moe::kStreamTokens : 16); }
 
 // ---------------------------------------------------------------- linear
 
@@ -216,12 +235,12 @@ LinearWork linear_carve(const moe_linear_cfg& c, int64_t T, bool back, void* ws,
   LinearWork L{};
   L.x = source(v, f32, x, ld_x, T, K);
   L.w = source(v, f32, w, K, N, K);
-  size_t part = part_bytes(moe::kNT, T, N, K, f32);
+  size_t part = part_bytes(T, N, K, f32);
   if (back) {
     if (c.act == MOE_ACT_NONE) L.dy = source(v, f32, dy, ld_dy, T, N);
     else L.dz = v.take<bf16_t>(planes_bytes(f32, T, N));
-    part = std::max(part, part_bytes(moe::kNN, T, K, N, f32));
-    part = std::max(part, part_bytes(moe::kTN, N, K, T, f32));
+    part = std::max(part, part_bytes(T, K, N, f32));
+    part = std::max(part, part_bytes(N, K, T, f32));
     L.sums = v.take<float>(moe::dense_colsum_bytes(T, N));
   }
   L.part = v.take<float>(part);
@@ -257,19 +276,19 @@ FfnWork ffn_carve(const moe_ffn_cfg& c, int64_t T, bool back, void* ws, const vo
   F.wu = source(v, f32, wu, H, I, H);
   F.wd = source(v, f32, wd, I, H, I);
   F.mid = v.take<bf16_t>(planes_bytes(f32, T, I));
-  size_t part = part_bytes(moe::kNT, T, I, H, f32, 1, 1);
+  size_t part = part_bytes(T, I, H, f32, 1, 1);
   if (back) {
     F.dy = source(v, f32, dy, ld_dy, T, H);
     F.dg = v.take<bf16_t>(planes_bytes(f32, T, I));
     F.du = v.take<bf16_t>(planes_bytes(f32, T, I));
     F.g = v.take<float>(size_t(T) * size_t(padded(I)) * sizeof(float));
     F.u = v.take<float>(size_t(T) * size_t(padded(I)) * sizeof(float));
-    part = std::max(part, part_bytes(moe::kNN, T, I, H, f32));
-    part = std::max(part, part_bytes(moe::kNN, T, H, I, f32, 2));
-    part = std::max(part, part_bytes(moe::kTN, I, H, T, f32));
-    part = std::max(part, part_bytes(moe::kTN, H, I, T, f32));
+    part = std::max(part, part_bytes(T, I, H, f32));
+    part = std::max(part, part_bytes(T, H, I, f32, 2));
+    part = std::max(part, part_bytes(I, H, T, f32, 1, 0, 3));
+    part = std::max(part, part_bytes(H, I, T, f32, 1, 0, 3));
   } else {
-    part = std::max(part, part_bytes(moe::kNT, T, H, I, f32));
+    part = std::max(part, part_bytes(T, H, I, f32));
   }
   F.part = v.take<float>(part);
   F.bytes = v.used;
@@ -367,10 +386,16 @@ int moe_linear_forward(const moe_linear_cfg* cfg, int64_t T, const void* x, int6
   if ((rc = check_device()) != MOE_OK) return rc;
   const bool f32 = cfg->dtype == MOE_F32;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  Mat X, W;
-  MOE_TRY(operand(L.x, f32, X, direct(L.x), st));
-  MOE_TRY(operand(L.w, f32, W, direct(L.w), st));
-  moe::DenseArgs g = product(T, N, K, L.part, moe::kEpiOut, f32);
+  if (streams(T, f32)) {
+    const moe::DenseStreamArgs a{x,    w,    nullptr,     bias, residual, y,
+                                 ld_x, ld_residual, ld_y, int(T), N, K, cfg->act};
+    MOE_TRY(moe::launch_dense_stream(a, f32, st));
+    return MOE_OK;
+  }
+  Operands ops(f32);
+  const Mat X = ops.add(L.x), W = ops.add(L.w);
+  MOE_TRY(ops.lay_out(st));
+  moe::DenseArgs g = product(T, N, K, moe::kEpiOut, f32);
   add_segments(g, f32, X, W);
   g.epi.act = cfg->act;
   g.epi.bias = bias;
@@ -378,7 +403,7 @@ int moe_linear_forward(const moe_linear_cfg* cfg, int64_t T, const void* x, int6
   g.epi.ld_residual = ld_residual;
   g.epi.out = y;
   g.epi.ld_out = ld_y;
-  MOE_TRY(moe::launch_dense(g, moe::kNT, st));
+  MOE_TRY(launch(g, moe::kNT, L.part, st));
   return MOE_OK;
 }
 
@@ -401,16 +426,18 @@ int moe_linear_backward(const moe_linear_cfg* cfg, int64_t T, const void* x, int
   if ((rc = check_device()) != MOE_OK) return rc;
   const bool f32 = cfg->dtype == MOE_F32, plain = cfg->act == MOE_ACT_NONE;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  Mat X, W, DZ;
-  if (!plain || dw != nullptr) MOE_TRY(operand(L.x, f32, X, direct(L.x), st));
-  if (!plain || dx != nullptr) MOE_TRY(operand(L.w, f32, W, direct(L.w), st));
+  Mat X{}, W{}, DZ{};
+  Operands ops(f32);
+  if (!plain || dw != nullptr) X = ops.add(L.x);
+  if (!plain || dx != nullptr) W = ops.add(L.w);
+  if (plain && (dx != nullptr || dw != nullptr)) DZ = ops.add(L.dy);
+  MOE_TRY(ops.lay_out(st));
   if (plain) {
-    if (dx != nullptr || dw != nullptr) MOE_TRY(operand(L.dy, f32, DZ, direct(L.dy), st));
     if (dbias != nullptr)
       MOE_TRY(moe::launch_dense_colsum(dy, ld_dy, f32 ? 0 : 1, 0, T, N, dbias, f32, L.sums, st));
   } else {
     DZ = planes_at(f32, L.dz, T, N);
-    moe::DenseArgs g = product(T, N, K, L.part, moe::kEpiActBack, f32);
+    moe::DenseArgs g = product(T, N, K, moe::kEpiActBack, f32);
     add_segments(g, f32, X, W);
     g.epi.act = cfg->act;
     g.epi.bias = bias;
@@ -418,23 +445,23 @@ int moe_linear_backward(const moe_linear_cfg* cfg, int64_t T, const void* x, int
     g.epi.ld_dy = ld_dy;
     g.epi.p0 = L.dz;
     stage_to(g.epi, DZ, T);
-    MOE_TRY(moe::launch_dense(g, moe::kNT, st));
+    MOE_TRY(launch(g, moe::kNT, L.part, st));
     if (dbias != nullptr)
       MOE_TRY(moe::launch_dense_colsum(L.dz, DZ.ld, f32 ? 3 : 1, T * DZ.ld, T, N, dbias, f32, L.sums, st));
   }
   if (dx != nullptr) {
-    moe::DenseArgs g = product(T, K, N, L.part, moe::kEpiOut, f32);
+    moe::DenseArgs g = product(T, K, N, moe::kEpiOut, f32);
     add_segments(g, f32, DZ, W);
     g.epi.out = dx;
     g.epi.ld_out = ld_dx;
-    MOE_TRY(moe::launch_dense(g, moe::kNN, st));
+    MOE_TRY(launch(g, moe::kNN, L.part, st));
   }
   if (dw != nullptr) {
-    moe::DenseArgs g = product(N, K, T, L.part, moe::kEpiOut, f32);
+    moe::DenseArgs g = product(N, K, T, moe::kEpiOut, f32);
     add_segments(g, f32, DZ, X);
     g.epi.out = dw;
     g.epi.ld_out = K;
-    MOE_TRY(moe::launch_dense(g, moe::kTN, st));
+    MOE_TRY(launch(g, moe::kTN, L.part, st));
   }
   return MOE_OK;
 }
@@ -459,26 +486,32 @@ int moe_ffn_forward(const moe_ffn_cfg* cfg, int64_t T, const void* x, int64_t ld
   if ((rc = check_device()) != MOE_OK) return rc;
   const bool f32 = cfg->dtype == MOE_F32;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  Mat X, WG, WU, WD;
-  MOE_TRY(operand(F.x, f32, X, direct(F.x), st));
+  if (streams(T, f32)) {
+    const moe::DenseStreamArgs up{x, w_gate, w_up, nullptr, nullptr, F.mid, ld_x, 0, I, int(T), I, H, cfg->act};
+    MOE_TRY(moe::launch_dense_stream(up, f32, st));
+    const moe::DenseStreamArgs down{F.mid, w_down, nullptr, nullptr,     residual, y,
+                                    I,     ld_residual, ld_y, int(T), H,        I, MOE_ACT_NONE};
+    MOE_TRY(moe::launch_dense_stream(down, f32, st));
+    return MOE_OK;
+  }
+  Operands ops(f32);
   const bool both = direct(F.wg) && direct(F.wu);  // the dual product reads both with one stride
-  MOE_TRY(operand(F.wg, f32, WG, both, st));
-  MOE_TRY(operand(F.wu, f32, WU, both, st));
-  MOE_TRY(operand(F.wd, f32, WD, direct(F.wd), st));
+  const Mat X = ops.add(F.x), WG = ops.add(F.wg, both), WU = ops.add(F.wu, both), WD = ops.add(F.wd);
+  MOE_TRY(ops.lay_out(st));
   const Mat MID = planes_at(f32, F.mid, T, I);
-  moe::DenseArgs g = product(T, I, H, F.part, moe::kEpiGated, f32);
+  moe::DenseArgs g = product(T, I, H, moe::kEpiGated, f32);
   add_segments(g, f32, X, WG, &WU);
   g.epi.act = cfg->act;
   g.epi.p0 = F.mid;
   stage_to(g.epi, MID, T);
-  MOE_TRY(moe::launch_dense(g, moe::kNT, st));
-  g = product(T, H, I, F.part, moe::kEpiOut, f32);
+  MOE_TRY(launch(g, moe::kNT, F.part, st));
+  g = product(T, H, I, moe::kEpiOut, f32);
   add_segments(g, f32, MID, WD);
   g.epi.residual = residual;
   g.epi.ld_residual = ld_residual;
   g.epi.out = y;
   g.epi.ld_out = ld_y;
-  MOE_TRY(moe::launch_dense(g, moe::kNT, st));
+  MOE_TRY(launch(g, moe::kNT, F.part, st));
   return MOE_OK;
 }
 
@@ -502,24 +535,22 @@ int moe_ffn_backward(const moe_ffn_cfg* cfg, int64_t T, const void* x, int64_t l
   if ((rc = check_device()) != MOE_OK) return rc;
   const bool f32 = cfg->dtype == MOE_F32;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  Mat X, WG, WU, WD, DY;
+  Operands ops(f32);
   const bool both = direct(F.wg) && direct(F.wu);
-  MOE_TRY(operand(F.x, f32, X, direct(F.x), st));
-  MOE_TRY(operand(F.wg, f32, WG, both, st));
-  MOE_TRY(operand(F.wu, f32, WU, both, st));
-  MOE_TRY(operand(F.wd, f32, WD, direct(F.wd), st));
-  MOE_TRY(operand(F.dy, f32, DY, direct(F.dy), st));
+  const Mat X = ops.add(F.x), WG = ops.add(F.wg, both), WU = ops.add(F.wu, both), WD = ops.add(F.wd),
+            DY = ops.add(F.dy);
+  MOE_TRY(ops.lay_out(st));
   const Mat MID = planes_at(f32, F.mid, T, I), DG = planes_at(f32, F.dg, T, I), DU = planes_at(f32, F.du, T, I);
   // The projections again, kept in float32: with bfloat16 the slope and the
   // product would carry a rounding of their own on top of the staged operands'.
-  moe::DenseArgs g = product(T, I, H, F.part, moe::kEpiKeep, f32);
+  moe::DenseArgs g = product(T, I, H, moe::kEpiKeep, f32);
   add_segments(g, f32, X, WG, &WU);
   g.epi.g = F.g;
   g.epi.u = F.u;
   stage_to(g.epi, MID, T);
-  MOE_TRY(moe::launch_dense(g, moe::kNT, st));
+  MOE_TRY(launch(g, moe::kNT, F.part, st));
   // the middle's gradient, and from it the projections' and the middle itself
-  g = product(T, I, H, F.part, moe::kEpiGatedBack, f32);
+  g = product(T, I, H, moe::kEpiGatedBack, f32);
   add_segments(g, f32, DY, WD);
   g.epi.act = cfg->act;
   g.epi.g = F.g;
@@ -528,22 +559,23 @@ int moe_ffn_backward(const moe_ffn_cfg* cfg, int64_t T, const void* x, int64_t l
   g.epi.p1 = F.du;
   g.epi.p2 = F.mid;
   stage_to(g.epi, MID, T);
-  MOE_TRY(moe::launch_dense(g, moe::kNN, st));
-  g = product(T, H, I, F.part, moe::kEpiOut, f32);
+  MOE_TRY(launch(g, moe::kNN, F.part, st));
+  g = product(T, H, I, moe::kEpiOut, f32);
   add_segments(g, f32, DG, WG);
   add_segments(g, f32, DU, WU);
   g.epi.out = dx;
   g.epi.ld_out = ld_dx;
-  MOE_TRY(moe::launch_dense(g, moe::kNN, st));
+  MOE_TRY(launch(g, moe::kNN, F.part, st));
   const struct { const Mat &a, &b; int rows, cols; void* out; } grads[3] = {
       {DG, X, I, H, dw_gate}, {DU, X, I, H, dw_up}, {DY, MID, H, I, dw_down}};
-  for (const auto& w : grads) {
-    g = product(w.rows, w.cols, T, F.part, moe::kEpiOut, f32);
-    add_segments(g, f32, w.a, w.b);
-    g.epi.out = w.out;
-    g.epi.ld_out = w.cols;
-    MOE_TRY(moe::launch_dense(g, moe::kTN, st));
+  moe::DenseGroup group{};
+  for (int i = 0; i < 3; ++i) {
+    group.g[i] = product(grads[i].rows, grads[i].cols, T, moe::kEpiOut, f32);
+    add_segments(group.g[i], f32, grads[i].a, grads[i].b);
+    group.g[i].epi.out = grads[i].out;
+    group.g[i].epi.ld_out = grads[i].cols;
   }
+  MOE_TRY(moe::launch_dense(group, 3, moe::kTN, F.part, st));
   return MOE_OK;
 }
 

@@ -158,9 +158,11 @@ def test_binding_refusals():
     with pytest.raises(ValueError, match="dtype"):
         moe.linear_forward(cfg, x.float(), w, y, None)
     with pytest.raises(ValueError, match="required"):
-        moe.linear_forward(cfg, x, None, y, None)
+        moe.linear_forward(cfg, None, w, y, None)
     with pytest.raises(ValueError, match="required"):
-        moe._ffn_weights(moe.make_ffn_cfg(64, 32), x.dtype, {"w_gate": w, "w_up": w})
+        moe.norm_forward(moe.make_norm_cfg(64), None, x, {"w_pre": w[0]}, x, x)
+    with pytest.raises(ValueError, match="required"):
+        moe._ffn_weights(moe.make_ffn_cfg(64, 32), x.dtype, {"w_up": w, "w_down": w})
     with pytest.raises(ValueError, match="contiguous"):
         moe._rows(torch.empty((64, 4), dtype=x.dtype, device="meta").T, "x", x.dtype, 4, 64)
     with pytest.raises(moe.MoeError):
