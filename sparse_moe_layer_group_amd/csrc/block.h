@@ -147,21 +147,10 @@ template <bool WHOLE> MOE_DEV void store8(bf16_t* row, int c, int n, const float
   }
 }
 
-// sum over the wave in a fixed order, every lane gets it: lane moves within
-// 16-lane rows by DPP, the last two steps by shuffles
+// v plus another lane's v (a move within 16-lane rows; every source is inside)
 template <int CTRL> MOE_DEV float add_dpp(float v) {
-  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
+  return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
 }
-MOE_DEV float wave_total(float v) {
-  v = add_dpp<0xb1>(v);   // lane ^ 1
-  v = add_dpp<0x4e>(v);   // lane ^ 2
-  v = add_dpp<0x124>(v);  // row_ror:4
-  v = add_dpp<0x128>(v);  // row_ror:8
-  v += __shfl_xor(v, 16, kWave);
-  v += __shfl_xor(v, 32, kWave);
-  return v;
-}
-
 // ---------------------------------------------------------------- norm (norm_kernels.hip)
 
 // One call's arguments; row strides in elements.  Absent tensors are NULL.
@@ -176,7 +165,7 @@ struct NormArgs {
   int64_t ld_residual, ld_branch, ld_u, ld_h, ld_du, ld_dh, ld_dr, ld_db;
   int64_t T;
   int H, gate_rows, layer;           // gate_rows 0: no gate
-  int workers, options;              // set by the launchers
+  int workers, options, partials;    // set by the launchers
   float eps, scale;
 };
 int norm_backward_workers(int64_t T, int H);

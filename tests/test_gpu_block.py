@@ -212,7 +212,7 @@ def test_ffn_with_one_unaligned_projection():
 NORM = [  # T, hidden, pad, gate_rows
     (1, 1, 0, 1), (1, 64, 0, 0), (5, 3, 1, 5), (9, 512, 0, 3), (40, 513, 3, 1), (64, 1000, 8, 16), (30, 1024, 0, 30),
     (33, 1025, 0, 11), (700, 1030, 2, 7), (600, 2048, 0, 200), (300, 7168, 0, 300), (515, 4100, 4, 103),
-    (20, 8192, 0, 4), (7, 8200, 1, 7), (6, 16384, 0, 2),
+    (20, 8192, 0, 4), (7, 8200, 1, 7), (6, 16384, 0, 2), (21, 256, 3, 7), (12, 1536, 5, 4), (1100, 72, 1, 1100),
 ]
 
 
