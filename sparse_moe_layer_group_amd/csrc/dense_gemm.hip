@@ -105,14 +105,15 @@ MOE_DEV void store_f32(float* p, const float (&v)[8]) {
 template <bool INSIDE, int R>
 MOE_DEV void load_rows(const DenseEpi& e, const void* p, int64_t ld, int64_t m, int step, int n, float (&v)[R][8]) {
   const int end = INSIDE ? n + 8 : e.N;
+  const int64_t first = m * ld, next = step * ld;  // one wide product for all rows
   if (e.f32) {
 #pragma unroll
-    for (int k = 0; k < R; ++k) load8<INSIDE>(static_cast<const float*>(p) + (m + k * step) * ld, n, end, v[k]);
+    for (int k = 0; k < R; ++k) load8<INSIDE>(static_cast<const float*>(p) + (first + k * next), n, end, v[k]);
   } else {
     u32x4 raw[R];
 #pragma unroll
     for (int k = 0; k < R; ++k)
-      raw[k] = load8_raw<INSIDE>(static_cast<const bf16_t*>(p) + (m + k * step) * ld, n, end);
+      raw[k] = load8_raw<INSIDE>(static_cast<const bf16_t*>(p) + (first + k * next), n, end);
 #pragma unroll
     for (int k = 0; k < R; ++k) unpack8(raw[k], v[k]);
   }
@@ -136,7 +137,7 @@ MOE_DEV void dense_epilogue(const DenseEpi& e, int64_t m, int step, int n, float
   if (MODE == kEpiGatedBack) {
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      const int64_t o = (m + k * step) * e.ld_p + n;
+      const int64_t o = m * e.ld_p + n + k * (step * e.ld_p);
       load8<true>(e.g + o, 0, 8, x[k]);
       load8<true>(e.u + o, 0, 8, u[k]);
     }
@@ -168,19 +169,19 @@ MOE_DEV void dense_epilogue(const DenseEpi& e, int64_t m, int step, int n, float
         for (int i = 0; i < 8; ++i) v[k][i] += x[k][i];
     }
     const int end = INSIDE ? n + 8 : e.N;
+    const int64_t first = m * e.ld_out, next = step * e.ld_out;
     if (e.f32) {
 #pragma unroll
-      for (int k = 0; k < R; ++k) store8<INSIDE>(static_cast<float*>(e.out) + (m + k * step) * e.ld_out, n, end, v[k]);
+      for (int k = 0; k < R; ++k) store8<INSIDE>(static_cast<float*>(e.out) + (first + k * next), n, end, v[k]);
     } else {
 #pragma unroll
-      for (int k = 0; k < R; ++k)
-        store8<INSIDE>(static_cast<bf16_t*>(e.out) + (m + k * step) * e.ld_out, n, end, v[k]);
+      for (int k = 0; k < R; ++k) store8<INSIDE>(static_cast<bf16_t*>(e.out) + (first + k * next), n, end, v[k]);
     }
     return;
   }
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    const int64_t o = (m + k * step) * e.ld_p + n;
+    const int64_t o = m * e.ld_p + n + k * (step * e.ld_p);
     if (MODE == kEpiActBack) {
       act_slopes(e.act, v[k]);
 #pragma unroll
@@ -638,18 +639,19 @@ template <typename TE> __global__ __launch_bounds__(256) void dense_pack_kernel(
 
 // Column sums.  A workgroup takes 256 columns, 8 a thread, and a range of rows
 // in 8 shares (share k: every eighth row from the k-th), joined in share order.
-constexpr int kSumRows = 256;  // rows of a workgroup
+constexpr int kSumRows = 64;  // rows of a workgroup
 template <typename TE>
 __global__ __launch_bounds__(256) void dense_colsum_kernel(const TE* src, int64_t ld, int n_planes, int64_t plane,
                                                            int64_t rows, int cols, float* part) {
   __shared__ float acc[8][256];
   const int lane = threadIdx.x & 31, share = threadIdx.x >> 5;
-  const int c = blockIdx.x * 256 + lane * 8;
-  const int64_t r0 = int64_t(blockIdx.y) * kSumRows;
+  const int c = blockIdx.y * 256 + lane * 8;
+  const int64_t r0 = int64_t(blockIdx.x) * kSumRows;
   const int64_t r1 = r0 + kSumRows < rows ? r0 + kSumRows : rows;
   float s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) s[i] = 0.f;
+#pragma unroll 8
   for (int64_t r = r0 + share; r < r1; r += 8)
     for (int p = 0; p < n_planes; ++p) {
       float v[8];
@@ -663,17 +665,28 @@ __global__ __launch_bounds__(256) void dense_colsum_kernel(const TE* src, int64_
   float t = 0.f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) t += acc[k][threadIdx.x];
-  const int col = blockIdx.x * 256 + threadIdx.x;
-  if (col < cols) part[int64_t(blockIdx.y) * cols + col] = t;
+  const int col = blockIdx.y * 256 + threadIdx.x;
+  if (col < cols) part[int64_t(blockIdx.x) * cols + col] = t;
 }
+// A workgroup takes 32 columns and 32 shares of the partial rows, joined in share order.
 template <typename TE>
-__global__ __launch_bounds__(256) void dense_colsum_join_kernel(const float* part, int64_t n, int cols, TE* out) {
-  const int col = blockIdx.x * 256 + threadIdx.x;
-  if (col >= cols) return;
+__global__ __launch_bounds__(1024) void dense_colsum_join_kernel(const float* part, int64_t n, int cols, TE* out) {
+  __shared__ float acc[32][33];
+  const int lane = threadIdx.x & 31, share = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
   float t = 0.f;
-#pragma unroll 8
-  for (int64_t i = 0; i < n; ++i) t += part[i * cols + col];
-  out[col] = from_f32<TE>(t);
+  if (col < cols) {
+#pragma unroll 4
+    for (int64_t i = share; i < n; i += 32) t += part[i * cols + col];
+  }
+  acc[share][lane] = t;
+  __syncthreads();
+  if (share == 0 && col < cols) {
+    t = 0.f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) t += acc[k][lane];
+    out[col] = from_f32<TE>(t);
+  }
 }
 
 // ---------------------------------------------------------------- launches
@@ -825,8 +838,8 @@ size_t dense_colsum_bytes(int64_t rows, int cols) {
 hipError_t launch_dense_colsum(const void* src, int64_t ld, int n_planes, int64_t plane, int64_t rows, int cols,
                                void* out, bool f32, float* part, hipStream_t st) {
   const int64_t chunks = (rows + kSumRows - 1) / kSumRows;
-  if (chunks > 65535) return hipErrorInvalidValue;  // entry points bound the rows
-  const dim3 grid((cols + 255) / 256, unsigned(chunks)), join((cols + 255) / 256);
+  // chunks lie along x: there are up to 2^18 of them
+  const dim3 grid(unsigned(chunks), (cols + 255) / 256), join((cols + 31) / 32);
   if (n_planes == 0)
     hipLaunchKernelGGL((dense_colsum_kernel<float>), grid, dim3(256), 0, st, static_cast<const float*>(src), ld, 1,
                        int64_t(0), rows, cols, part);
@@ -836,10 +849,10 @@ hipError_t launch_dense_colsum(const void* src, int64_t ld, int n_planes, int64_
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   if (f32)
-    hipLaunchKernelGGL((dense_colsum_join_kernel<float>), join, dim3(256), 0, st, part, chunks, cols,
+    hipLaunchKernelGGL((dense_colsum_join_kernel<float>), join, dim3(1024), 0, st, part, chunks, cols,
                        static_cast<float*>(out));
   else
-    hipLaunchKernelGGL((dense_colsum_join_kernel<bf16_t>), join, dim3(256), 0, st, part, chunks, cols,
+    hipLaunchKernelGGL((dense_colsum_join_kernel<bf16_t>), join, dim3(1024), 0, st, part, chunks, cols,
                        static_cast<bf16_t*>(out));
   return hipGetLastError();
 }

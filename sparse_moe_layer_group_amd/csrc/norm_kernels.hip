@@ -225,6 +225,11 @@ template <typename TE_, int NV_, bool ONE_WAVE_, bool LAYER_, bool WHOLE_> struc
   typedef TE_ TE;
   static constexpr int NV = NV_;
   static constexpr bool ONE_WAVE = ONE_WAVE_, LAYER = LAYER_, WHOLE = WHOLE_;
+  // backward: the parameters are read again for every row (from the caches)
+  // where keeping them would put other registers out to memory
+  static constexpr bool REREAD = !ONE_WAVE && (LAYER || !WHOLE || NV > 2 || sizeof(TE) == 4);
+  // ... and the next row is not kept in flight
+  static constexpr bool FETCH_AHEAD = NV <= 2;
 };
 
 // NormArgs::options, set by the launchers from the pointers given
@@ -236,7 +241,6 @@ int norm_options(const NormArgs& a) {
 }
 
 constexpr int kRowThreads = 512;  // most threads of a workgroup that shares a row
-constexpr int kBackThreads = 512;   // ... in the backward
 constexpr int kRowWaves = 4;  // waves (one row each) of a workgroup of one-wave workers
 
 }  // namespace
@@ -345,7 +349,7 @@ __global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kRowThreads) void no
 // their partial rows: gpart[2 w] is worker w's share of a row begun before its
 // range, gpart[2 w + 1] of one begun inside it and going on after it.
 template <class S>
-__global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kBackThreads) void norm_backward_kernel(NormArgs a) {
+__global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kRowThreads) void norm_backward_kernel(NormArgs a) {
   typedef typename S::TE TE;
   constexpr int NV = S::NV;
   constexpr bool ONE = S::ONE_WAVE;
@@ -366,14 +370,17 @@ __global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kBackThreads) void n
   const TE* dh = static_cast<const TE*>(a.dh);
   typedef Raw8<TE, S::WHOLE> Raw;
   constexpr int NB = S::LAYER ? NV : 1;  // vectors of what only the layer norm has
-  Raw wpost[NV], wpre[NV], gate[NV], bpost[NB];
+  constexpr int NP = S::REREAD ? 1 : NV;
+  Raw wpost_[NP], wpre_[NP], gate_[NP], bpost_[S::REREAD ? 1 : NB];
   float swpost[NV][8], swpre[NV][8], sgate[NV][8], sbpost[NB][8], sbpre[NB][8];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    take(wpost[j], a.w_post, c, j, true);
-    take(wpre[j], a.w_pre, c, j, true);
-    gate[j].fill(true);
-    if (S::LAYER) take(bpost[j], a.b_post, c, j, false);
+    if (!S::REREAD) {
+      take(wpost_[j], a.w_post, c, j, true);
+      take(wpre_[j], a.w_pre, c, j, true);
+      gate_[j].fill(true);
+      if (S::LAYER) take(bpost_[j], a.b_post, c, j, false);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       swpost[j][i] = swpre[j][i] = sgate[j][i] = 0.f;
@@ -385,6 +392,18 @@ __global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kBackThreads) void n
   const int64_t t0 = worker_row(a.T, min(worker, a.workers), a.workers);
   const int64_t t1 = worker_row(a.T, min(worker + 1, a.workers), a.workers);
   int64_t group = -1, group_end = t0;
+  auto read_again = [&](const void* p, int j, bool one) __attribute__((always_inline)) {
+    Raw r;
+    take(r, p, c, j, one);
+    return r;
+  };
+  auto wpost = [&](int j) __attribute__((always_inline)) { return S::REREAD ? read_again(a.w_post, j, true) : wpost_[S::REREAD ? 0 : j]; };
+  auto wpre = [&](int j) __attribute__((always_inline)) { return S::REREAD ? read_again(a.w_pre, j, true) : wpre_[S::REREAD ? 0 : j]; };
+  auto bpost = [&](int j) __attribute__((always_inline)) { return S::REREAD ? read_again(a.b_post, j, false) : bpost_[S::REREAD ? 0 : j]; };
+  auto gate = [&](int j) __attribute__((always_inline)) {
+    return S::REREAD ? read_again(a.gate ? static_cast<const TE*>(a.gate) + group * H : nullptr, j, true)
+                     : gate_[S::REREAD ? 0 : j];
+  };
   // the gate row `group` ends at row `end` of the worker's range
   auto flush_gate = [&](int64_t end) {
     if (a.dgate == nullptr || group < 0) return;
@@ -421,7 +440,7 @@ __global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kBackThreads) void n
     if (du) du += a.ld_du;
     if (dh) dh += a.ld_dh;
   };
-  if (t0 < t1) fetch();
+  if (S::FETCH_AHEAD && t0 < t1) fetch();
   for (int64_t t = t0; t < t1; ++t) {
     int opt = a.options;  // read anew for every row, as in the forward
     asm volatile("" : "+s"(opt));
@@ -430,8 +449,9 @@ __global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kBackThreads) void n
       group = t / a.gate_rows;
       group_end = (group + 1) * a.gate_rows;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) gate[j].load(static_cast<const TE*>(a.gate) + group * H, c, j);
+      for (int j = 0; j < NV && !S::REREAD; ++j) gate_[j].load(static_cast<const TE*>(a.gate) + group * H, c, j);
     }
+    if (!S::FETCH_AHEAD) fetch();
     float q[NV][8], p[NV][8], e[NV][8], d[NV][8];  // u, then q; p; du, then e; dh, then a
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -439,11 +459,13 @@ __global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kBackThreads) void n
       fn[j].get(p[j]);
       dun[j].get(e[j]);
       dhn[j].get(d[j]);
-      wpost[j].pin();
-      wpre[j].pin();
-      gate[j].pin();
+      if (!S::REREAD) {
+        wpost_[j].pin();
+        wpre_[j].pin();
+        gate_[j].pin();
+      }
     }
-    if (t + 1 < t1) fetch();
+    if (S::FETCH_AHEAD && t + 1 < t1) fetch();
     float inv_f = 1.f;
     if (opt & kNormPost) inv_f = unit_row<S>(p, c, a.eps, rs);
     float s3 = 0.f, s4 = 0.f;  // row means of c and c p
@@ -455,9 +477,9 @@ __global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kBackThreads) void n
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float w[8], g[8], x[8];
-        wpost[j].get(w);
-        gate[j].get(g);
-        wpre[j].get(x);
+        wpost(j).get(w);
+        gate(j).get(g);
+        wpre(j).get(x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float ng = p[j][i] * w[i] * g[i], aw = d[j][i] * x[i];
@@ -477,7 +499,7 @@ __global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kBackThreads) void n
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           float x[8];
-          wpre[j].get(x);
+          wpre(j).get(x);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             swpre[j][i] = fmaf(d[j][i] * inv_u, q[j][i], swpre[j][i]);
@@ -491,8 +513,8 @@ __global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kBackThreads) void n
         float n[8], g[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) n[i] = p[j][i];
-        affine<S>(n, wpost[j], bpost[S::LAYER ? j : 0]);
-        gate[j].get(g);
+        affine<S>(n, wpost(j), bpost(S::LAYER ? j : 0));
+        gate(j).get(g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) q[j][i] = fmaf(n[i], g[i], a.scale * q[j][i]);
       }
@@ -502,7 +524,7 @@ __global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kBackThreads) void n
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           float w[8];
-          wpre[j].get(w);
+          wpre(j).get(w);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             swpre[j][i] = fmaf(d[j][i], q[j][i], swpre[j][i]);
@@ -530,9 +552,9 @@ __global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kBackThreads) void n
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) n[i] = p[j][i];
-      affine<S>(n, wpost[j], bpost[S::LAYER ? j : 0]);
-      gate[j].get(g);
-      wpost[j].get(w);
+      affine<S>(n, wpost(j), bpost(S::LAYER ? j : 0));
+      gate(j).get(g);
+      wpost(j).get(w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         sgate[j][i] = fmaf(e[j][i], n[i], sgate[j][i]);
@@ -596,16 +618,19 @@ __global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kBackThreads) void n
   }
 }
 
+// Worker of row t: the largest w with T w / workers <= t
+MOE_DEV int64_t row_worker(const NormArgs& a, int64_t t) { return ((t + 1) * a.workers - 1) / a.T; }
+
 // Joins the workgroups' partial rows in their order: blockIdx.y 0..3 the weight
-// gradients, 4 + g the gate row g.  A workgroup has 64 columns and 16 shares
-// of the rows (share k: rows k, k + 16, ...), added up share by share.
+// gradients, 4 + g the gate row g.  A workgroup has 64 columns and 16 shares of
+// the rows (share k: rows k, k + 16, ...), added up share by share.
 constexpr int kJoinShares = 16;
 template <typename TE>
 __global__ __launch_bounds__(64 * kJoinShares) void norm_join_kernel(NormArgs a) {
   __shared__ float acc[kJoinShares][64];
   const int lane = threadIdx.x & 63, share = threadIdx.x >> 6;
   const int col = blockIdx.x * 64 + lane;
-  const int64_t which = blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
+  const int which = blockIdx.y;
   TE* out;
   const float* src;
   int64_t first, last, step;
@@ -618,11 +643,8 @@ __global__ __launch_bounds__(64 * kJoinShares) void norm_join_kernel(NormArgs a)
     step = a.H;
   } else {
     const int64_t g = which - 4;
-    if (a.dgate == nullptr || g >= a.T / a.gate_rows) return;
-    const int64_t r0 = g * a.gate_rows, r1 = r0 + a.gate_rows;
-    // worker of row t: the largest w with T w / n <= t
-    first = ((r0 + 1) * a.workers - 1) / a.T;
-    last = (r1 * a.workers - 1) / a.T + 1;
+    first = row_worker(a, g * a.gate_rows);
+    last = row_worker(a, (g + 1) * a.gate_rows - 1) + 1;
     if (last - first == 1) return;  // one worker had the whole row and wrote it
     out = static_cast<TE*>(a.dgate) + g * a.H;
     src = a.gpart;
@@ -645,6 +667,21 @@ __global__ __launch_bounds__(64 * kJoinShares) void norm_join_kernel(NormArgs a)
   }
 }
 
+// The same for gate rows where there are many of them, each shared by a few
+// workers: blockIdx.y is worker b, for the gate row that began in its range and
+// goes on past it, if there is one.
+constexpr int kFewGates = 64;  // up to here the join above takes them
+template <typename TE> __global__ __launch_bounds__(256) void norm_gate_join_kernel(NormArgs a) {
+  const int col = blockIdx.x * 256 + threadIdx.x;
+  const int64_t b = blockIdx.y, end = worker_row(a.T, int(b) + 1, a.workers);
+  const int64_t g = end / a.gate_rows, r0 = g * a.gate_rows;
+  if (r0 == end || r0 < worker_row(a.T, int(b), a.workers) || col >= a.H) return;
+  const int64_t last = row_worker(a, r0 + a.gate_rows - 1);
+  float s = a.gpart[(2 * b + 1) * a.H + col];
+  for (int64_t w = b + 1; w <= last; ++w) s += a.gpart[2 * w * a.H + col];
+  (static_cast<TE*>(a.dgate) + g * a.H)[col] = from_f32<TE>(s);
+}
+
 // ---------------------------------------------------------------- launches
 
 namespace {
@@ -653,13 +690,12 @@ struct NormPlan {
   bool one_wave;
   int nv, threads;  // of a workgroup
 };
-NormPlan norm_plan(int H, bool back) {
+NormPlan norm_plan(int H) {
   if (H <= 1024) return {true, H <= 512 ? 1 : 2, 64 * kRowWaves};
   const int nv = H <= 2 * 8 * kRowThreads ? 2 : 4;
   return {false, nv, ((H + 8 * nv - 1) / (8 * nv) + 63) / 64 * 64};
 }
-static_assert(4 * 8 * kRowThreads >= kNormMaxHidden && 4 * 8 * kBackThreads >= kNormMaxHidden,
-              "the widest row fits a workgroup");
+static_assert(4 * 8 * kRowThreads >= kNormMaxHidden, "the widest row fits a workgroup");
 
 // F::launch<NormShape<...>> for the shape, kind and alignment of the call
 template <class F, typename TE, int NV, bool ONE> void pick_form(const NormArgs& a, const F& f) {
@@ -669,11 +705,11 @@ template <class F, typename TE, int NV, bool ONE> void pick_form(const NormArgs&
   else if (whole) f(NormShape<TE, NV, ONE, false, true>{});
   else f(NormShape<TE, NV, ONE, false, false>{});
 }
-template <class F, typename TE, int NV1, int NV2> void pick_shape(const NormArgs& a, const NormPlan& p, const F& f) {
+template <class F, typename TE> void pick_shape(const NormArgs& a, const NormPlan& p, const F& f) {
   if (p.one_wave && p.nv == 1) pick_form<F, TE, 1, true>(a, f);
   else if (p.one_wave) pick_form<F, TE, 2, true>(a, f);
-  else if (p.nv == NV1) pick_form<F, TE, NV1, false>(a, f);
-  else pick_form<F, TE, NV2, false>(a, f);
+  else if (p.nv == 2) pick_form<F, TE, 2, false>(a, f);
+  else pick_form<F, TE, 4, false>(a, f);
 }
 
 template <typename TE>
@@ -681,7 +717,7 @@ hipError_t launch_forward(const NormArgs& a, const NormPlan& p, unsigned grid, h
   auto f = [&](auto shape) {
     hipLaunchKernelGGL((norm_forward_kernel<decltype(shape)>), dim3(grid), dim3(p.threads), 0, st, a);
   };
-  pick_shape<decltype(f), TE, 2, 4>(a, p, f);
+  pick_shape<decltype(f), TE>(a, p, f);
   return hipGetLastError();
 }
 
@@ -690,15 +726,17 @@ hipError_t launch_backward(const NormArgs& a, const NormPlan& p, unsigned grid, 
   auto f = [&](auto shape) {
     hipLaunchKernelGGL((norm_backward_kernel<decltype(shape)>), dim3(grid), dim3(p.threads), 0, st, a);
   };
-  pick_shape<decltype(f), TE, 2, 4>(a, p, f);
+  pick_shape<decltype(f), TE>(a, p, f);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  const int64_t groups = a.dgate ? a.T / a.gate_rows : 0;
-  const int64_t jobs = 4 + groups;  // grid.y holds up to 65535 of them
-  const unsigned gy = unsigned(jobs < 32768 ? jobs : 32768), gz = unsigned((jobs + gy - 1) / gy);
   NormArgs join = a;
   join.partials = int(grid);
-  hipLaunchKernelGGL((norm_join_kernel<TE>), dim3((a.H + 63) / 64, gy, gz), dim3(64 * kJoinShares), 0, st, join);
+  const int64_t gates = a.dgate ? a.T / a.gate_rows : 0;
+  const unsigned jobs = 4 + unsigned(gates <= kFewGates ? gates : 0);
+  hipLaunchKernelGGL((norm_join_kernel<TE>), dim3((a.H + 63) / 64, jobs), dim3(64 * kJoinShares), 0, st, join);
+  // (a gate row of one token is one worker's, and a lone worker has them all)
+  if (gates > kFewGates && a.gate_rows > 1 && a.workers > 1)
+    hipLaunchKernelGGL((norm_gate_join_kernel<TE>), dim3((a.H + 255) / 256, a.workers - 1), dim3(256), 0, st, join);
   return hipGetLastError();
 }
 
@@ -707,15 +745,15 @@ hipError_t launch_backward(const NormArgs& a, const NormPlan& p, unsigned grid, 
 // Workers of the backward: enough for every CU, few enough that their partial
 // rows stay small beside the tokens' own rows.
 int norm_backward_workers(int64_t T, int H) {
-  const NormPlan p = norm_plan(H, true);
-  const int64_t most = p.one_wave ? 1024 : p.threads <= 256 ? 512 : 256;
+  const NormPlan p = norm_plan(H);
+  const int64_t most = p.one_wave ? (p.nv == 1 ? 2048 : 1024) : int64_t(256) * std::max(1, 512 / p.threads);
   return int(T < most ? T : most);
 }
 
 hipError_t launch_norm_forward(const NormArgs& args, bool bf16, hipStream_t st) {
   NormArgs a = args;
   a.options = norm_options(a);
-  const NormPlan p = norm_plan(a.H, false);
+  const NormPlan p = norm_plan(a.H);
   // every wave slot of the chip: workers hold their weights over their rows
   const int64_t most = p.one_wave ? 256 * 32 : 256 * (2048 / p.threads);
   a.workers = int(a.T < most ? a.T : most);
@@ -726,7 +764,7 @@ hipError_t launch_norm_forward(const NormArgs& args, bool bf16, hipStream_t st) 
 hipError_t launch_norm_backward(const NormArgs& args, bool bf16, hipStream_t st) {
   NormArgs a = args;
   a.options = norm_options(a);
-  const NormPlan p = norm_plan(a.H, true);
+  const NormPlan p = norm_plan(a.H);
   a.workers = norm_backward_workers(a.T, a.H);
   const unsigned grid = unsigned(p.one_wave ? (a.workers + kRowWaves - 1) / kRowWaves : a.workers);
   return bf16 ? launch_backward<bf16_t>(a, p, grid, st) : launch_backward<float>(a, p, grid, st);
