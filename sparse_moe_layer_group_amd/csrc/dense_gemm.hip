@@ -12,7 +12,7 @@
 //
 // Tiles.  Workgroup tile TM x TN, contraction in steps of 64 through two LDS
 // stages filled by buffer_load ... lds copies; four waves in 2 x 2, each
-// TM/2 x TN/2 in 32x32x16 MFMA blocks.  A k-contiguous operand is staged as
+// TM/2 x TN/2 in 16x16x32 MFMA blocks.  A k-contiguous operand is staged as
 // rows of 64 (chunk c of row r at c ^ (r & 7)), a k-slow one as k-rows of TM or
 // TN columns, read with the transposing ds_read_b64_tr_b16.
 //
@@ -44,28 +44,52 @@ typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 constexpr int kWaitAll = 0x0070;
 constexpr int wait_copies(int n) { return (n & 15) | ((n >> 4) << 14) | 0x70 | 0xf00; }
 
-// position of 16-byte chunk c in k-row r: the four k-rows of one transposed
-// read hit distinct banks
-MOE_DEV int kswz(int r, int c) { return c ^ ((r & 3) << 1); }
+// position of 16-byte chunk c in k-row r of RL columns: the eight k-rows that
+// two lane groups of a transposed read take together hit distinct banks
+template <int RL> MOE_DEV int kswz(int r, int c) {
+  return c ^ (RL >= 128 ? ((r & 3) << 1) ^ (r & 8) : ((r & 2) << 1) ^ ((r & 8) >> 2));
+}
 
 // 8 k of row `row` (k-contiguous stage of rows of 64)
 MOE_DEV bf16x8 row_frag(const bf16_t* st, int row, int chunk) {
   return *reinterpret_cast<const bf16x8*>(st + row * BK + ((chunk ^ (row & 7)) << 3));
 }
 
-// columns i0 .. i0+31, k kbase .. kbase+15 of a k-row stage of RL columns:
-// lane l gets column i0 + l%32, k = kbase + 8 (l/32) .. +7
+// columns i0 .. i0+15, k kbase .. kbase+31 of a k-row stage of RL columns:
+// lane l gets column i0 + l%16, k = kbase + 8 (l/16) .. +7
 template <int RL> MOE_DEV bf16x8 tr_frag(const bf16_t* st, int kbase, int i0, int lane) {
   const int g = lane >> 4, s = lane & 15;
-  const int col = i0 + 16 * (g & 1) + 4 * (s & 3);
+  const int col = i0 + 4 * (s & 3);
   v4i16 h[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int k = kbase + 8 * (g >> 1) + 4 * q + (s >> 2);
-    const bf16_t* p = st + k * RL + (kswz(k, col >> 3) << 3) + (col & 7);
+    const int k = kbase + 8 * g + 4 * q + (s >> 2);
+    const bf16_t* p = st + k * RL + (kswz<RL>(k, col >> 3) << 3) + (col & 7);
     h[q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)((__attribute__((address_space(3))) bf16_t*)p));
   }
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// acc += a b.  Written as assembly to update the accumulator where it lies: the
+// builtin's result may go to other registers, and with all 256 of them taken by
+// accumulators this compiler moves 190 of them about and spills 12 a step.  It
+// does not know of a wait that such a product needs, so one is made before the
+// first and after the last (settle).  Operands come straight from LDS reads,
+// whose waits it does know of.
+MOE_DEV void multiply_add(f32x4& acc, bf16x8 a, bf16x8 b) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+}
+// Between other accesses to accumulators and products, either way round: no
+// instruction on an accumulator passes it.
+template <int M, int N> MOE_DEV void settle(f32x4 (&acc)[M][N]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) asm volatile("" : "+a"(acc[i][j]));
+    if (k == 0) asm volatile("s_nop 15\n\ts_nop 7");
+  }
 }
 
 // ---------------------------------------------------------------- epilogue
@@ -127,12 +151,15 @@ template <int MODE, bool INSIDE> MOE_DEV void load_bias(const DenseEpi& e, int n
 }
 
 // Columns n .. n+7 (n % 8 == 0, n < N) of the R rows m, m + step, ...: their
-// loads are issued together, then the arithmetic, then their stores.
-template <int MODE, bool INSIDE, int R>
-MOE_DEV void dense_epilogue(const DenseEpi& e, int64_t m, int step, int n, float (&v)[R][8], float (&u)[R][8],
+// loads are issued together, then the arithmetic, then their stores.  RESIDUAL:
+// e.residual is there.  (Asked at both its load and its use, it leaves the
+// compiler a path with loads that nothing waited for, and it then waits for all
+// memory operations, the stores too, before the next rows.)
+template <int MODE, bool INSIDE, bool RESIDUAL, int R>
+MOE_DEV void dense_rows(const DenseEpi& e, int64_t m, int step, int n, float (&v)[R][8], float (&u)[R][8],
                             const float (&b)[1][8]) {
   float x[R][8];  // residual, upstream gradient or gate projection
-  if (MODE == kEpiOut && e.residual) load_rows<INSIDE, R>(e, e.residual, e.ld_residual, m, step, n, x);
+  if (RESIDUAL) load_rows<INSIDE, R>(e, e.residual, e.ld_residual, m, step, n, x);
   if (MODE == kEpiActBack) load_rows<INSIDE, R>(e, e.dy, e.ld_dy, m, step, n, x);
   if (MODE == kEpiGatedBack) {
 #pragma unroll
@@ -162,7 +189,7 @@ MOE_DEV void dense_epilogue(const DenseEpi& e, int64_t m, int step, int n, float
 #pragma unroll
       for (int k = 0; k < R; ++k) act_values(e.act, v[k]);
     }
-    if (e.residual) {
+    if (RESIDUAL) {
 #pragma unroll
       for (int k = 0; k < R; ++k)
 #pragma unroll
@@ -211,6 +238,13 @@ MOE_DEV void dense_epilogue(const DenseEpi& e, int64_t m, int step, int n, float
       store_planes(e, e.p2, o, s);
     }
   }
+}
+
+template <int MODE, bool INSIDE, int R>
+MOE_DEV void dense_epilogue(const DenseEpi& e, int64_t m, int step, int n, float (&v)[R][8], float (&u)[R][8],
+                            const float (&b)[1][8]) {
+  if (MODE == kEpiOut && e.residual) dense_rows<MODE, INSIDE, true, R>(e, m, step, n, v, u, b);
+  else dense_rows<MODE, INSIDE, false, R>(e, m, step, n, v, u, b);
 }
 
 // One element's planes
@@ -314,7 +348,7 @@ MOE_DEV void scatter_sum(float (&v)[8], int share) {
 template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_kernel(DenseGroup group) {
   constexpr int TM = S::TM, TN = S::TN;
   constexpr bool A_ROWS = S::LAYOUT != kTN, B_ROWS = S::LAYOUT == kNT;  // k-contiguous operands
-  constexpr int MB = TM / 64, NB = TN / 64;          // 32 x 32 blocks of a wave
+  constexpr int MB = TM / 32, NB = TN / 32;          // 16 x 16 blocks of a wave
   constexpr int ASTAGE = TM * BK, BSTAGE = TN * BK;  // elements
   constexpr int ACP = TM / 32, BCP = TN / 32;        // 1 KB copies of a wave per step
   constexpr int NCOL = S::DUAL ? TN / 2 : TN;        // output columns of a tile
@@ -351,7 +385,7 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
     } else {
       constexpr int KR = 512 / TM, LPR = TM / 8;  // k-rows of a copy, lanes of a k-row
       const int kr = KR * (ACP * wave + i) + lane / LPR;
-      aoff[i] = uint32_t(kr * lda + kswz(kr, lane % LPR) * 8) * 2u;
+      aoff[i] = uint32_t(kr * lda + kswz<TM>(kr, lane % LPR) * 8) * 2u;
     }
   }
 #pragma unroll
@@ -363,7 +397,7 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
     } else {
       constexpr int KR = 512 / TN, LPR = TN / 8;
       const int kr = KR * (BCP * wave + i) + lane / LPR;
-      boff[i] = uint32_t(kr * ldb + kswz(kr, lane % LPR) * 8) * 2u;
+      boff[i] = uint32_t(kr * ldb + kswz<TN>(kr, lane % LPR) * 8) * 2u;
     }
   }
   // Sources of the next step to be copied.  A resource starts at the step's
@@ -425,18 +459,17 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
     copy_to_lds_async16(s.b, B_ROWS ? boff[i] | s.beyond : boff[i], Bs + stage * BSTAGE + (BCP * wave + i) * 512);
   };
 
-  f32x16 acc[MB][NB];
+  f32x4 acc[MB][NB];
 #pragma unroll
   for (int i = 0; i < MB; ++i)
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  settle(acc);
 
   // first staged B row (or column) of the wave's block j: a dual wave takes the
   // same columns of both matrices
   auto bcol = [&](int j) {
-    return S::DUAL ? (j / (NB / 2)) * (TN / 2) + wn * (TN / 4) + 32 * (j % (NB / 2)) : wn * (TN / 2) + 32 * j;
+    return S::DUAL ? (j / (NB / 2)) * (TN / 2) + wn * (TN / 4) + 16 * (j % (NB / 2)) : wn * (TN / 2) + 16 * j;
   };
   struct Frags { bf16x8 a[MB], b[NB]; };
   // fragment idx of slice s of the step in A's stage sa and B's stage sb
@@ -444,24 +477,26 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
     const bf16_t* a = As + sa * ASTAGE;
     const bf16_t* b = Bs + sb * BSTAGE;
     if (idx < NB) {
-      if (B_ROWS) f.b[idx] = row_frag(b, bcol(idx) + (lane & 31), 2 * s + (lane >> 5));
-      else f.b[idx] = tr_frag<TN>(b, 16 * s, bcol(idx), lane);
+      if (B_ROWS) f.b[idx] = row_frag(b, bcol(idx) + (lane & 15), 4 * s + (lane >> 4));
+      else f.b[idx] = tr_frag<TN>(b, 32 * s, bcol(idx), lane);
     } else {
       const int i = idx - NB;
-      if (A_ROWS) f.a[i] = row_frag(a, wm * (TM / 2) + 32 * i + (lane & 31), 2 * s + (lane >> 5));
-      else f.a[i] = tr_frag<TM>(a, 16 * s, wm * (TM / 2) + 32 * i, lane);
+      if (A_ROWS) f.a[i] = row_frag(a, wm * (TM / 2) + 16 * i + (lane & 15), 4 * s + (lane >> 4));
+      else f.a[i] = tr_frag<TM>(a, 32 * s, wm * (TM / 2) + 16 * i, lane);
     }
   };
-  // MFMAs of one slice with the reads of the slice two ahead and half of one
-  // operand's copies spread evenly between them, in this order
+  // MFMAs of one slice (32 of k) with the reads of the next and one operand's
+  // copies spread between them, in this order.  The reads are over some MFMAs
+  // before the slice is, so that they have landed when it ends.
   auto slice = [&](const Frags& f, Frags& nx, int sa, int sb, int s, auto copy, auto copies) {
     constexpr int NQ = MB * NB, NR = MB + NB, NC = decltype(copies)::value;
+    constexpr int RQ = NQ >= 16 ? NQ - NQ / 8 : NQ / 2;  // MFMAs with reads
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       const int i = q / NB, j = q % NB;
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
+      multiply_add(acc[i][j], f.b[j], f.a[i]);
 #pragma unroll
-      for (int r = q * NR / NQ; r < (q + 1) * NR / NQ; ++r) read(nx, r, sa, sb, s);
+      for (int r = q * NR / RQ; r < (q + 1) * NR / RQ && r < NR; ++r) read(nx, r, sa, sb, s);
 #pragma unroll
       for (int r = q * NC / NQ; r < (q + 1) * NC / NQ; ++r) copy(r);
       __builtin_amdgcn_sched_barrier(0);
@@ -480,38 +515,32 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
   static_assert(D * (ACP + BCP) < 64, "vmcnt has 6 bits");
   __builtin_amdgcn_s_waitcnt(wait_copies((D - 1) * (ACP + BCP)));  // the first step's
   __builtin_amdgcn_s_barrier();
-  Frags f[4];  // of the four slices
+  Frags f[2];  // of the two slices
 #pragma unroll
-  for (int q = 0; q < MB + NB; ++q) {
-    read(f[0], q, 0, 0, 0);
-    read(f[1], q, 0, 0, 1);
-  }
+  for (int q = 0; q < MB + NB; ++q) read(f[0], q, 0, 0, 0);
   int sa = 0, sb = 0;  // the step's stages; A's for step kt + D is the one before sa
   for (int kt = 0; kt < nk; ++kt) {
     const int sa1 = sa == D ? 0 : sa + 1, sb1 = sb == D - 1 ? 0 : sb + 1, sad = sa == 0 ? D : sa - 1;
     const Step next = this_step();  // kt + D
-    const std::integral_constant<int, ACP / 2> half_a{};
-    const std::integral_constant<int, BCP / 2> half_b{};
-    slice(f[0], f[2], sa, sb, 2, [&](int r) { copy_a(r, next, sad); }, half_a);
-    slice(f[1], f[3], sa, sb, 3, [&](int r) { copy_a(ACP / 2 + r, next, sad); }, half_a);
+    slice(f[0], f[1], sa, sb, 1, [&](int r) { copy_a(r, next, sad); }, std::integral_constant<int, ACP>{});
     // this wave's copies of the next step have landed (those of later steps are
     // in flight) and its reads of this one are done; behind the barrier everyone's
     __builtin_amdgcn_s_waitcnt(wait_copies((D - 1) * ACP + (D - 2) * BCP) & ~0xf00);
     __builtin_amdgcn_s_barrier();
-    slice(f[2], f[0], sa1, sb1, 0, [&](int r) { copy_b(r, next, sb); }, half_b);
-    slice(f[3], f[1], sa1, sb1, 1, [&](int r) { copy_b(BCP / 2 + r, next, sb); }, half_b);
+    slice(f[1], f[0], sa1, sb1, 0, [&](int r) { copy_b(r, next, sb); }, std::integral_constant<int, BCP>{});
     sa = sa1;
     sb = sb1;
     advance();
   }
+  settle(acc);
   __builtin_amdgcn_s_waitcnt(kWaitAll);  // no copy left in flight
   __syncthreads();
 
   // ---- epilogue.  B is the MFMA's first operand, so accumulator v of lane l
-  // is row l%32, column 8 (v/4) + 4 (l/32) + v%4: four columns in a row.  Each
-  // wave passes 32 rows of its columns at a time through LDS (float32), so that
-  // a lane has 8 consecutive columns of a row.
-  constexpr int WC = 32 * NB;             // staged columns of a wave
+  // is row l%16, column 4 (l/16) + v: four columns in a row.  Each wave passes
+  // 32 rows of its columns at a time through LDS (float32), so that a lane has
+  // 8 consecutive columns of a row.
+  constexpr int WC = 16 * NB;             // staged columns of a wave
   constexpr int OC = S::DUAL ? WC / 2 : WC;  // output columns of a wave
   constexpr int PITCH = WC * 4 + 16;      // bytes
   static_assert(4 * 32 * PITCH <= S::LDS, "the staging rows fit the stages");
@@ -549,18 +578,15 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
   constexpr int AHEAD = 32 / RPI < 4 ? 32 / RPI : 4;  // rows at a time where all are inside
   const bool whole = m0 + TM <= g.M && n0 + NCOL <= g.N;
 #pragma unroll 1
-  for (int blk = 0; blk < MB; ++blk) {
+  for (int blk = 0; blk < MB / 2; ++blk) {
     const int64_t mrow = m0 + wm * (TM / 2) + 32 * blk;
     if (mrow >= g.M) break;  // uniform
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-      if (i != blk) continue;  // uniform: the accumulators are indexed at compile time, the rest is one loop
+      if (i / 2 != blk) continue;  // uniform: the accumulators are indexed at compile time, the rest is one loop
 #pragma unroll
       for (int j = 0; j < NB; ++j)
-#pragma unroll
-        for (int v = 0; v < 16; v += 4)
-          *(lds_f32x4*)(slot + (lane & 31) * PITCH + 4 * (32 * j + 2 * v + 4 * (lane >> 5))) =
-              f32x4{acc[i][j][v], acc[i][j][v + 1], acc[i][j][v + 2], acc[i][j][v + 3]};
+        *(lds_f32x4*)(slot + (16 * (i & 1) + (lane & 15)) * PITCH + 4 * (16 * j + 4 * (lane >> 4))) = acc[i][j];
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     if (whole) {
