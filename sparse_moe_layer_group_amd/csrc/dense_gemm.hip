@@ -401,63 +401,91 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
     }
   }
   // Sources of the next step to be copied.  A resource starts at the step's
-  // first element; `end` is what it spans, counted from the segment's first
-  // step (k-contiguous: to the end of the tile's last row, rows ending at a
-  // multiple of 8) or from its own (k-slow: the k-rows that are left).
+  // first element; its span is counted from the segment's first step for a
+  // k-contiguous operand (to the end of the tile's last row, rows ending at a
+  // multiple of 8) and from its own for a k-slow one (the k-rows that are left).
   const int kpad = (K + 7) & ~7;
   const int64_t cols_a = ((g.M + 7) & ~int64_t(7)) - m0, cols_b = ((int64_t(g.N) + 7) & ~int64_t(7)) - n0;
   const int rows_a = int(std::min<int64_t>(TM, g.M - m0)), rows_b = min(S::DUAL ? TN / 2 : TN, g.N - n0);
   const uint32_t end_a = A_ROWS ? uint32_t(((rows_a - 1) * lda + kpad) * 2) : uint32_t((63 * lda + cols_a) * 2);
   const uint32_t end_b = B_ROWS ? uint32_t(((rows_b - 1) * ldb + kpad) * 2) : uint32_t((63 * ldb + cols_b) * 2);
   const int64_t step_a = (A_ROWS ? BK : BK * lda) * 2, step_b = (B_ROWS ? BK : BK * ldb) * 2;
-  int seg = s0 / per_segment, kk = (s0 - seg * per_segment) * BK, left = nk;
+  int seg = s0 / per_segment, kk = (s0 - seg * per_segment) * BK;
+  int left = nk, kend;  // steps after this segment's, and where this workgroup's range of it ends
   const char *pa, *pb;
   uint32_t span_a, span_b;
-  auto spans = [&]() __attribute__((always_inline)) {
-    const int krows = min(BK, K - kk);
-    span_a = A_ROWS ? end_a - uint32_t(kk) * 2u : end_a - uint32_t((BK - krows) * lda * 2);
-    span_b = B_ROWS ? end_b - uint32_t(kk) * 2u : end_b - uint32_t((BK - krows) * ldb * 2);
-  };
+  __amdgpu_buffer_rsrc_t ra, rb;
   auto seek = [&]() __attribute__((always_inline)) {
     const int64_t k = kk;
+    const int steps = min(left, per_segment - kk / BK);
+    left -= steps;
+    kend = min(K, kk + steps * BK);
     const bf16_t* qb = S::DUAL && wave >= 2 ? g.b2[seg] : g.b[seg];
     pa = reinterpret_cast<const char*>(g.a[seg] + (A_ROWS ? m0 * lda + k : k * lda + m0));
     pb = reinterpret_cast<const char*>(qb + (B_ROWS ? n0 * ldb + k : k * ldb + n0));
-    spans();
-  };
-  seek();
-  struct Step {
-    __amdgpu_buffer_rsrc_t a, b;
-    uint32_t beyond;
-  };
-  auto this_step = [&]() {
-    Step s;
-    s.a = buffer_rsrc(pa, span_a);
-    s.b = buffer_rsrc(pb, span_b);
-    s.beyond = kk + achunk * 8 >= kpad ? kBeyond : 0u;
-    return s;
-  };
-  // (past the last step the position stays, and the last step is copied again:
-  // every step has its copies)
-  auto advance = [&]() __attribute__((always_inline)) {
-    if (--left <= 0) return;
-    kk += BK;
-    if (kk >= K) {
-      kk = 0;
-      ++seg;
-      seek();
-    } else {
-      pa += step_a;
-      pb += step_b;
-      spans();
+    span_a = A_ROWS ? end_a - uint32_t(kk) * 2u : end_a;
+    span_b = B_ROWS ? end_b - uint32_t(kk) * 2u : end_b;
+    // (as assembly: an `and` is made in every step, whether this is called or not)
+    const uint32_t within = ~kBeyond;
+    if (A_ROWS) {
+#pragma unroll
+      for (int i = 0; i < ACP; ++i) asm volatile("v_and_b32 %0, %1, %0" : "+v"(aoff[i]) : "s"(within));
+    }
+    if (B_ROWS) {
+#pragma unroll
+      for (int i = 0; i < BCP; ++i) asm volatile("v_and_b32 %0, %1, %0" : "+v"(boff[i]) : "s"(within));
     }
   };
-  auto copy_a = [&](int i, const Step& s, int stage) {
-    copy_to_lds_async16(s.a, A_ROWS ? aoff[i] | s.beyond : aoff[i], As + stage * ASTAGE + (ACP * wave + i) * 512);
+  // a step that is not a whole one of the segment's range: the next segment's
+  // first, the range's last with fewer than 64 of k, or one past the last, of
+  // which nothing is there (every step has its copies)
+  auto edge = [&]() __attribute__((always_inline)) {
+    if (kk >= kend) {
+      if (left > 0) {
+        kk = 0;
+        ++seg;
+        seek();
+      } else {
+        kend = 0;
+        span_a = span_b = 0;
+      }
+    }
+    if (kk < kend && kk + BK > K) {
+      const uint32_t beyond = kk + achunk * 8 >= kpad ? kBeyond : 0u;
+      if (A_ROWS) {
+#pragma unroll
+        for (int i = 0; i < ACP; ++i) aoff[i] |= beyond;
+      } else {
+        span_a = end_a - uint32_t((kk + BK - K) * lda * 2);
+      }
+      if (B_ROWS) {
+#pragma unroll
+        for (int i = 0; i < BCP; ++i) boff[i] |= beyond;
+      } else {
+        span_b = end_b - uint32_t((kk + BK - K) * ldb * 2);
+      }
+    }
+    ra = buffer_rsrc(pa, span_a);
+    rb = buffer_rsrc(pb, span_b);
   };
-  auto copy_b = [&](int i, const Step& s, int stage) {
-    copy_to_lds_async16(s.b, B_ROWS ? boff[i] | s.beyond : boff[i], Bs + stage * BSTAGE + (BCP * wave + i) * 512);
+  // the next step, in pieces
+  auto advance = [&](int piece) __attribute__((always_inline)) {
+    if (piece == 0) {
+      pa += step_a;
+      if (A_ROWS) span_a -= 2 * BK;
+      ra = buffer_rsrc(pa, span_a);
+    } else {
+      pb += step_b;
+      if (B_ROWS) span_b -= 2 * BK;
+      rb = buffer_rsrc(pb, span_b);
+      kk += BK;
+    }
   };
+  seek();
+  edge();
+  // copy i of the step into the stage that begins at element `stage`
+  auto copy_a = [&](int i, int stage) { copy_to_lds_async16(ra, aoff[i], As + stage + (ACP * wave + i) * 512); };
+  auto copy_b = [&](int i, int stage) { copy_to_lds_async16(rb, boff[i], Bs + stage + (BCP * wave + i) * 512); };
 
   f32x4 acc[MB][NB];
 #pragma unroll
@@ -472,10 +500,10 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
     return S::DUAL ? (j / (NB / 2)) * (TN / 2) + wn * (TN / 4) + 16 * (j % (NB / 2)) : wn * (TN / 2) + 16 * j;
   };
   struct Frags { bf16x8 a[MB], b[NB]; };
-  // fragment idx of slice s of the step in A's stage sa and B's stage sb
+  // fragment idx of slice s of the step whose stages begin at elements sa and sb
   auto read = [&](Frags& f, int idx, int sa, int sb, int s) {
-    const bf16_t* a = As + sa * ASTAGE;
-    const bf16_t* b = Bs + sb * BSTAGE;
+    const bf16_t* a = As + sa;
+    const bf16_t* b = Bs + sb;
     if (idx < NB) {
       if (B_ROWS) f.b[idx] = row_frag(b, bcol(idx) + (lane & 15), 4 * s + (lane >> 4));
       else f.b[idx] = tr_frag<TN>(b, 32 * s, bcol(idx), lane);
@@ -485,32 +513,39 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
       else f.a[i] = tr_frag<TM>(a, 32 * s, wm * (TM / 2) + 16 * i, lane);
     }
   };
-  // MFMAs of one slice (32 of k) with the reads of the next and one operand's
-  // copies spread between them, in this order.  The reads are over some MFMAs
-  // before the slice is, so that they have landed when it ends.
-  auto slice = [&](const Frags& f, Frags& nx, int sa, int sb, int s, auto copy, auto copies) {
-    constexpr int NQ = MB * NB, NR = MB + NB, NC = decltype(copies)::value;
-    constexpr int RQ = NQ >= 16 ? NQ - NQ / 8 : NQ / 2;  // MFMAs with reads
+  // MFMAs of one slice (32 of k) with the reads of the next slice, one operand's
+  // copies and the preparation of the next step spread between them, in this
+  // order: 16 cycles of an MFMA hide three other instructions, so no two of
+  // these share one where there are enough.  The reads begin first and end
+  // after three quarters, so that they have landed when the slice ends.
+  auto slice = [&](const Frags& f, Frags& nx, int sa, int sb, int s, auto copy, auto copies, auto prepare) {
+    constexpr int NQ = MB * NB, NR = MB + NB, NC = decltype(copies)::value, MOST = NQ * 3 / 4;
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       const int i = q / NB, j = q % NB;
       multiply_add(acc[i][j], f.b[j], f.a[i]);
 #pragma unroll
-      for (int r = q * NR / RQ; r < (q + 1) * NR / RQ && r < NR; ++r) read(nx, r, sa, sb, s);
+      for (int r = 0; r < NR; ++r)
+        if (q == r * MOST / NR) read(nx, r, sa, sb, s);
 #pragma unroll
-      for (int r = q * NC / NQ; r < (q + 1) * NC / NQ; ++r) copy(r);
+      for (int r = 0; r < NC; ++r)
+        if (q == r * MOST / NC + (NQ >= 16 ? 1 : 0)) copy(r);
+#pragma unroll
+      for (int r = 0; r < 3; ++r)
+        if (q == MOST + r * (NQ - MOST) / 3) prepare(r);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
 
 #pragma unroll
   for (int st = 0; st < D; ++st) {
-    const Step s = this_step();
 #pragma unroll
-    for (int i = 0; i < ACP; ++i) copy_a(i, s, st);
+    for (int i = 0; i < ACP; ++i) copy_a(i, st * ASTAGE);
 #pragma unroll
-    for (int i = 0; i < BCP; ++i) copy_b(i, s, st);
-    advance();
+    for (int i = 0; i < BCP; ++i) copy_b(i, st * BSTAGE);
+    advance(0);
+    advance(1);
+    if (kk + BK > kend) edge();
   }
   static_assert(D * (ACP + BCP) < 64, "vmcnt has 6 bits");
   __builtin_amdgcn_s_waitcnt(wait_copies((D - 1) * (ACP + BCP)));  // the first step's
@@ -518,19 +553,27 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
   Frags f[2];  // of the two slices
 #pragma unroll
   for (int q = 0; q < MB + NB; ++q) read(f[0], q, 0, 0, 0);
-  int sa = 0, sb = 0;  // the step's stages; A's for step kt + D is the one before sa
+  // stages of the step before, of this one and the next (A), of this and the next (B)
+  int sa0 = D * ASTAGE, sa = 0, sa1 = ASTAGE, sb = 0, sb1 = BSTAGE;
   for (int kt = 0; kt < nk; ++kt) {
-    const int sa1 = sa == D ? 0 : sa + 1, sb1 = sb == D - 1 ? 0 : sb + 1, sad = sa == 0 ? D : sa - 1;
-    const Step next = this_step();  // kt + D
-    slice(f[0], f[1], sa, sb, 1, [&](int r) { copy_a(r, next, sad); }, std::integral_constant<int, ACP>{});
+    // (the copies are of step kt + D)
+    slice(f[0], f[1], sa, sb, 1, [&](int r) { copy_a(r, sa0); }, std::integral_constant<int, ACP>{}, [](int) {});
     // this wave's copies of the next step have landed (those of later steps are
     // in flight) and its reads of this one are done; behind the barrier everyone's
     __builtin_amdgcn_s_waitcnt(wait_copies((D - 1) * ACP + (D - 2) * BCP) & ~0xf00);
     __builtin_amdgcn_s_barrier();
-    slice(f[1], f[0], sa1, sb1, 0, [&](int r) { copy_b(r, next, sb); }, std::integral_constant<int, BCP>{});
-    sa = sa1;
-    sb = sb1;
-    advance();
+    slice(f[1], f[0], sa1, sb1, 0, [&](int r) { copy_b(r, sb); }, std::integral_constant<int, BCP>{}, [&](int r) {
+      if (r < 2) {
+        advance(r);
+      } else {
+        sa0 = sa;
+        sa = sa1;
+        sa1 = sa1 == D * ASTAGE ? 0 : sa1 + ASTAGE;
+        sb = sb1;
+        sb1 = sb1 == (D - 1) * BSTAGE ? 0 : sb1 + BSTAGE;
+      }
+    });
+    if (kk + BK > kend) edge();
   }
   settle(acc);
   __builtin_amdgcn_s_waitcnt(kWaitAll);  // no copy left in flight
