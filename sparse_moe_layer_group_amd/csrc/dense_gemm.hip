@@ -522,7 +522,7 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
     constexpr int NQ = MB * NB, NR = MB + NB, NC = decltype(copies)::value, MOST = NQ * 3 / 4;
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      const int i = q / NB, j = q % NB;
+      const int i = q / NB, j = i & 1 ? NB - 1 - q % NB : q % NB;  // one operand stays at every turn
       multiply_add(acc[i][j], f.b[j], f.a[i]);
 #pragma unroll
       for (int r = 0; r < NR; ++r)
