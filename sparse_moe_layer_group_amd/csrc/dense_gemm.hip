@@ -154,13 +154,20 @@ template <int MODE, bool INSIDE> MOE_DEV void load_bias(const DenseEpi& e, int n
 // loads are issued together, then the arithmetic, then their stores.  RESIDUAL:
 // e.residual is there.  (Asked at both its load and its use, it leaves the
 // compiler a path with loads that nothing waited for, and it then waits for all
-// memory operations, the stores too, before the next rows.)
+// memory operations, the stores too, before the next rows.)  early: the rows of
+// the residual or upstream gradient, where they were loaded before.
 template <int MODE, bool INSIDE, bool RESIDUAL, int R>
 MOE_DEV void dense_rows(const DenseEpi& e, int64_t m, int step, int n, float (&v)[R][8], float (&u)[R][8],
-                            const float (&b)[1][8]) {
+                        const float (&b)[1][8], const u32x4* early = nullptr) {
   float x[R][8];  // residual, upstream gradient or gate projection
-  if (RESIDUAL) load_rows<INSIDE, R>(e, e.residual, e.ld_residual, m, step, n, x);
-  if (MODE == kEpiActBack) load_rows<INSIDE, R>(e, e.dy, e.ld_dy, m, step, n, x);
+  if (early != nullptr) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) unpack8(early[k], x[k]);
+  } else if (RESIDUAL) {
+    load_rows<INSIDE, R>(e, e.residual, e.ld_residual, m, step, n, x);
+  } else if (MODE == kEpiActBack) {
+    load_rows<INSIDE, R>(e, e.dy, e.ld_dy, m, step, n, x);
+  }
   if (MODE == kEpiGatedBack) {
 #pragma unroll
     for (int k = 0; k < R; ++k) {
@@ -596,7 +603,7 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
   float bias[1][8];
   if (g.split == 1) load_bias<S::MODE, false>(g.epi, n, bias);
   // R rows of this lane from row r of the staged 32, which are rows mrow ...
-  auto finish = [&](int64_t mrow, int r, auto inside, auto rows) __attribute__((always_inline)) {
+  auto finish = [&](int64_t mrow, int r, auto inside, auto rows, const u32x4* early) __attribute__((always_inline)) {
     constexpr int R = decltype(rows)::value;
     float v[R][8], u[R][8];
 #pragma unroll
@@ -610,7 +617,9 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
 #pragma unroll
         for (int i = 0; i < 4; ++i) { v[k][4 * h + i] = p[i]; u[k][4 * h + i] = q[i]; }
       }
-    if (g.split == 1) {
+    if (early != nullptr) {
+      dense_rows<S::MODE, true, S::MODE == kEpiOut, R>(g.epi, mrow + r, RPI, n, v, u, bias, early);
+    } else if (g.split == 1) {
       dense_epilogue<S::MODE, decltype(inside)::value, R>(g.epi, mrow + r, RPI, n, v, u, bias);
     } else {
 #pragma unroll
@@ -623,9 +632,29 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
   };
   constexpr int AHEAD = 32 / RPI < 4 ? 32 / RPI : 4;  // rows at a time where all are inside
   const bool whole = m0 + TM <= g.M && n0 + NCOL <= g.N;
+  const int64_t row0 = m0 + wm * (TM / 2);
+  // Where a bfloat16 matrix joins in, its rows for the next 32 are loaded before
+  // these are finished: a workgroup that has its CU to itself has nothing else
+  // to do while they come.
+  constexpr bool JOINS = TM == 256 && (S::MODE == kEpiOut || S::MODE == kEpiActBack);
+  constexpr int TURNS = 32 / (RPI * AHEAD);
+  const bf16_t* join = static_cast<const bf16_t*>(S::MODE == kEpiOut ? g.epi.residual : g.epi.dy);
+  const int64_t ld_join = S::MODE == kEpiOut ? g.epi.ld_residual : g.epi.ld_dy;
+  const bool early = JOINS && whole && join != nullptr && !g.epi.f32 && g.split == 1;
+  u32x4 next[TURNS][AHEAD];
+  auto fetch = [&](int blk) __attribute__((always_inline)) {
+    const bf16_t* first = join + (row0 + 32 * blk + lane / LPR) * ld_join + n;
+#pragma unroll
+    for (int t = 0; t < TURNS; ++t)
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) next[t][k] = load8_raw<true>(first + RPI * (AHEAD * t + k) * ld_join, 0, 8);
+  };
+  if constexpr (JOINS) {
+    if (early) fetch(0);
+  }
 #pragma unroll 1
   for (int blk = 0; blk < MB / 2; ++blk) {
-    const int64_t mrow = m0 + wm * (TM / 2) + 32 * blk;
+    const int64_t mrow = row0 + 32 * blk;
     if (mrow >= g.M) break;  // uniform
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
@@ -635,14 +664,29 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void dense_gemm_ker
         *(lds_f32x4*)(slot + (16 * (i & 1) + (lane & 15)) * PITCH + 4 * (16 * j + 4 * (lane >> 4))) = acc[i][j];
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (whole) {
+    if (early) {
+      if constexpr (JOINS) {
+        u32x4 now[TURNS][AHEAD];
+#pragma unroll
+        for (int t = 0; t < TURNS; ++t)
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) {
+            now[t][k] = next[t][k];
+            asm volatile("" : "+v"(now[t][k]));  // these are moved, not the ones on their way
+          }
+        fetch(min(blk + 1, MB / 2 - 1));
+#pragma unroll
+        for (int t = 0; t < TURNS; ++t)
+          finish(mrow, lane / LPR + RPI * AHEAD * t, std::true_type{}, std::integral_constant<int, AHEAD>{}, now[t]);
+      }
+    } else if (whole) {
 #pragma unroll 1
       for (int r = lane / LPR; r < 32; r += RPI * AHEAD)
-        finish(mrow, r, std::true_type{}, std::integral_constant<int, AHEAD>{});
+        finish(mrow, r, std::true_type{}, std::integral_constant<int, AHEAD>{}, nullptr);
     } else {
 #pragma unroll 1
       for (int r = lane / LPR; r < 32; r += RPI)
-        if (mrow + r < g.M && n < g.N) finish(mrow, r, std::false_type{}, std::integral_constant<int, 1>{});
+        if (mrow + r < g.M && n < g.N) finish(mrow, r, std::false_type{}, std::integral_constant<int, 1>{}, nullptr);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
