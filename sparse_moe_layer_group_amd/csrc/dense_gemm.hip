@@ -310,7 +310,7 @@ template <int MODE> MOE_DEV void dense_epilogue1(const DenseEpi& e, int64_t m, i
 template <int LAYOUT_, int MODE_, int TM_, int TN_> struct DenseShape {
   static constexpr int LAYOUT = LAYOUT_, MODE = MODE_, TM = TM_, TN = TN_;
   static constexpr bool DUAL = MODE == kEpiGated || MODE == kEpiKeep;
-  static constexpr int AHEAD = ((TM == 256 ? 160 : 80) * 1024 - TM * BK * 2) / ((TM + TN) * BK * 2);
+  static constexpr int AHEAD = ((TM == 256 ? 160 : TN == 32 ? 70 : 80) * 1024 - TM * BK * 2) / ((TM + TN) * BK * 2);
   static constexpr int LDS = ((AHEAD + 1) * TM + AHEAD * TN) * BK * 2;
   static_assert(AHEAD >= 2, "B's stage is refilled a step before its use");
 };
@@ -810,13 +810,13 @@ __global__ __launch_bounds__(1024) void dense_colsum_join_kernel(const float* pa
 namespace {
 
 struct DensePlan {
-  int tile;         // TM = TN (dual: at least 128 columns)
+  int tile;         // TN, and TM from 64 on (dual: at least 128 columns)
   int split, steps;
 };
 
 int64_t tiles_of(int64_t M, int64_t N, int dual, int tile) {
-  const int64_t nc = dual ? std::max(tile, 128) / 2 : tile;
-  return ((M + tile - 1) / tile) * ((N + nc - 1) / nc);
+  const int64_t nc = dual ? std::max(tile, 128) / 2 : tile, rows = std::max(tile, 64);
+  return ((M + rows - 1) / rows) * ((N + nc - 1) / nc);
 }
 
 // What a step of the contraction takes on a CU, and what a tile takes besides
@@ -829,18 +829,24 @@ struct TileCost {
   int tile, per_cu;
   double step[2], once;
 };
-constexpr TileCost kTileCosts[] = {{256, 1, {1.25, 1.25}, 14.0}, {128, 2, {0.53, 0.95}, 4.0}, {64, 2, {0.30, 0.41}, 2.5}};
+constexpr TileCost kTileCosts[] = {{256, 1, {1.25, 1.25}, 14.0}, {128, 2, {0.53, 0.95}, 4.0},
+                                   {64, 2, {0.30, 0.41}, 2.5}, {32, 2, {0.25, 0.35}, 2.5}};
 constexpr double kJoinOnce = 5.5, kJoinBytesPerUs = 4.5e6;  // of a split contraction's second launch
 
 // Tile and contraction split of a product: what costs least.  The large tile
 // moves half the operand bytes of the next for the same product and reaches
 // the highest rate, the small ones and the split fill the chip where there are
 // few tiles, and every split is paid for with its sums' way through memory.
-DensePlan dense_plan(int64_t M, int N, int64_t K, int segments, int dual, int count) {
+// narrow: the 64 x 32 tile is there, for forward products of few tokens, whose
+// weights should pass through as many CUs as there are (50 tokens by 7168 rows
+// of 2048: 11.3 us against 13.5 by 64 x 64 and as much by a split).
+bool narrow(int layout, int mode) { return layout == kNT && mode == kEpiOut; }
+DensePlan dense_plan(int64_t M, int N, int64_t K, int segments, int dual, int count, bool narrow) {
   const int64_t steps = (K + BK - 1) / BK * segments;
   DensePlan best{};
   double least = 0;
   for (const TileCost& c : kTileCosts) {
+    if (c.tile == 32 && !narrow) break;
     const int64_t tiles = tiles_of(M, N, dual, c.tile) * count;
     for (int split : {1, 2, 3, 4, 6, 8, 12, 16}) {
       if (split > 1 && (steps < 4 * split || tiles * split > 1024)) break;
@@ -875,12 +881,20 @@ template <class S> hipError_t launch_shape(const DenseGroup& group, int count, h
   return hipGetLastError();
 }
 
+template <int LAYOUT, int MODE> hipError_t launch_narrow(const DenseGroup& group, int count, hipStream_t st) {
+  if constexpr (LAYOUT == kNT && MODE == kEpiOut)
+    return launch_shape<DenseShape<LAYOUT, MODE, 64, 32>>(group, count, st);
+  else
+    return hipErrorInvalidValue;
+}
+
 template <int LAYOUT, int MODE>
 hipError_t launch_mode(const DenseGroup& group, int count, const DensePlan& p, hipStream_t st) {
   constexpr bool DUAL = MODE == kEpiGated || MODE == kEpiKeep;
   const hipError_t err = p.tile == 256   ? launch_shape<DenseShape<LAYOUT, MODE, 256, 256>>(group, count, st)
                          : p.tile == 128 ? launch_shape<DenseShape<LAYOUT, MODE, 128, 128>>(group, count, st)
-                                         : launch_shape<DenseShape<LAYOUT, MODE, 64, DUAL ? 128 : 64>>(group, count, st);
+                         : p.tile == 64  ? launch_shape<DenseShape<LAYOUT, MODE, 64, DUAL ? 128 : 64>>(group, count, st)
+                                         : launch_narrow<LAYOUT, MODE>(group, count, st);
   if (err != hipSuccess || p.split == 1) return err;
   int64_t pieces = 0;
   for (int i = 0; i < count; ++i) pieces = std::max(pieces, group.g[i].M * ((group.g[i].N + 7) / 8));
@@ -901,7 +915,10 @@ int64_t part_floats(const DensePlan& p, int64_t M, int N, int dual) {
 }  // namespace
 
 size_t dense_part_bytes(int64_t M, int N, int64_t K, int segments, int dual, int count) {
-  return size_t(count) * size_t(part_floats(dense_plan(M, N, K, segments, dual, count), M, N, dual)) * sizeof(float);
+  int64_t floats = 0;
+  for (bool thin : {false, true})
+    floats = std::max(floats, part_floats(dense_plan(M, N, K, segments, dual, count, thin && !dual), M, N, dual));
+  return size_t(count) * size_t(floats) * sizeof(float);
 }
 
 hipError_t launch_dense(const DenseGroup& args, int count, int layout, float* part, hipStream_t st) {
@@ -910,7 +927,7 @@ hipError_t launch_dense(const DenseGroup& args, int count, int layout, float* pa
   const DenseArgs& f = group.g[0];
   if (f.M <= 0 || f.N <= 0) return hipSuccess;
   const int mode = f.epi.mode;
-  const DensePlan p = dense_plan(f.M, f.N, f.K, f.segments, f.dual, count);
+  const DensePlan p = dense_plan(f.M, f.N, f.K, f.segments, f.dual, count, narrow(layout, mode));
   if (p.split > 1 && part == nullptr) return hipErrorInvalidValue;
   for (int i = 0; i < count; ++i) {
     DenseArgs& g = group.g[i];
