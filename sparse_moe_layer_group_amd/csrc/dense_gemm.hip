@@ -702,11 +702,12 @@ template <int MODE, int SHARES> __global__ __launch_bounds__(256) void dense_joi
   constexpr bool DUAL = MODE == kEpiGated || MODE == kEpiKeep;
   const DenseArgs& g = group_args(group);
   const int nc = (g.N + 7) / 8;
-  const int64_t id = (int64_t(blockIdx.x) * 256 + threadIdx.x) / SHARES;
+  // (a product of at most 1024 tiles: its pieces fit 32 bits)
+  const uint32_t id = (blockIdx.x * 256 + threadIdx.x) / SHARES, row = id / uint32_t(nc);
   const int share = threadIdx.x % SHARES;
-  const int64_t m = id / nc;
+  const int64_t m = row;
   if (m >= g.M) return;  // all of a piece's lanes
-  const int n = int(id - m * nc) * 8;
+  const int n = int(id - row * nc) * 8;
   float v[1][8], u[1][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[0][i] = u[0][i] = 0.f;
