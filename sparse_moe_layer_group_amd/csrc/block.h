@@ -160,7 +160,7 @@ struct NormArgs {
   void *u, *h;                       // forward outputs
   void *d_residual, *d_branch;       // backward outputs
   void *dw_post, *db_post, *dw_pre, *db_pre, *dgate;
-  float* part;                       // [4][workers][H]: per-worker sums of dw_post, db_post, dw_pre, db_pre
+  float* part;                       // [4][workgroups][H]: sums of dw_post, db_post, dw_pre, db_pre
   float* gpart;                      // [2 workers][H]: of the gate rows that workers share
   int64_t ld_residual, ld_branch, ld_u, ld_h, ld_du, ld_dh, ld_dr, ld_db;
   int64_t T;

@@ -13,6 +13,11 @@
 // as they lie, 16 bytes a lane at any alignment; a 16x16x32 MFMA takes 16 rows
 // of them against 16 tokens.  float32 operands are split in registers into
 // three bfloat16 parts (exactly) and multiplied as six MFMAs.
+//
+// Measured, one token, bfloat16: 2 x 2048 rows of 7168 in 13 us = 4.5 TB/s,
+// 7168 rows of 2048 in 8.6 us = 3.4 TB/s; a launch that reads nothing takes 3.5.
+// From 17 tokens on the loads of the tokens themselves, which every workgroup
+// repeats, are what bounds it (32 tokens through both: 42 us, by tiles 32).
 #include "block.h"
 
 namespace moe {

@@ -18,15 +18,26 @@
 //
 // Memory-bound: 4 (forward) or 6 (backward) rows move per token and about 14
 // or 40 operations an element.  A row therefore stays in registers from its
-// load to its stores, 8 consecutive elements a thread, so every element is
-// read and written once however many statistics the row needs.  A row of up
-// to 1024 is one wave's, and needs no barrier; a longer row is one
-// workgroup's, of as many waves as it has 512s.  A worker (that wave or
-// workgroup) takes a contiguous range of rows: it keeps the norm weights in
-// registers over them, has its next row's loads in flight while it works on
-// the present one, and in the backward adds its columns' weight gradients up
-// in registers, one partial row a worker, which a second kernel joins in
-// worker order (deterministic, no atomics).
+// load to its stores, vectors of 8 consecutive elements a thread, so every
+// element is read and written once however many statistics the row needs.  A
+// row of up to 1024 is one wave's, and needs no barrier; a longer row is one
+// workgroup's, of up to 512 threads with two vectors each (past 8192 four).
+// A worker (that wave or workgroup) takes a contiguous range of rows: it keeps
+// the norm weights in registers over them, has its next row's loads in flight
+// while it works on the present one, and in the backward adds its columns'
+// weight gradients up in registers, one partial row a workgroup, which a
+// second kernel joins in workgroup order (deterministic, no atomics).  Where
+// the backward's registers are short (layer norm, float32, ragged and wide
+// rows), the weights are read again for every row, from the caches, and past
+// 8192 the next row is not fetched ahead: 4096 rows of 7168 with a layer norm
+// 340 -> 130 us, 2048 of 16384 with an RMS norm 722 -> 170 us.
+//
+// Measured: forward, 8192 rows of 7168 in bfloat16, 96 us = 4.9 TB/s, what a
+// large copy reaches on this card (5.0); one row 4 us, a launch's latency.
+// Backward, 4096 rows of 7168 in bfloat16, RMS: 80 us = 4.4 TB/s and 6 us for
+// the join; as a layer norm 130 us, float32 165 us.  777 rows of 1001 in
+// float32, layer norm: 10 + 5 us.  Of the backward's 80 us the sums' barriers
+// and the column gradients' arithmetic are what is above the copy's 70.
 #include "block.h"
 
 namespace moe {
