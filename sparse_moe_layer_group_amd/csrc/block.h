@@ -216,10 +216,12 @@ struct DenseArgs {
 };
 // Up to three products of one layout, mode, contraction and M N go in one
 // launch (the gate, up and down matrices' gradients).
-constexpr int kMaxGroup = 3;
+constexpr int kMaxGroup = 4;  // these and a data gradient
 struct DenseGroup { DenseArgs g[kMaxGroup]; };
 size_t dense_part_bytes(int64_t M, int N, int64_t K, int segments, int dual, int count);
 hipError_t launch_dense(const DenseGroup& group, int count, int layout, float* part, hipStream_t st);
+hipError_t launch_dense_gradients(const DenseArgs& data, const DenseGroup& weights, int count, float* part,
+                                  hipStream_t st);
 
 // ---------------------------------------------------------------- few tokens (dense_stream.hip)
 

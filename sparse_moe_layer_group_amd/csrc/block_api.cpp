@@ -450,20 +450,23 @@ int moe_linear_backward(const moe_linear_cfg* cfg, int64_t T, const void* x, int
     if (dbias != nullptr)
       MOE_TRY(moe::launch_dense_colsum(L.dz, DZ.ld, f32 ? 3 : 1, T * DZ.ld, T, N, dbias, f32, L.sums, st));
   }
+  moe::DenseArgs data{};
+  moe::DenseGroup weights{};
   if (dx != nullptr) {
-    moe::DenseArgs g = product(T, K, N, moe::kEpiOut, f32);
-    add_segments(g, f32, DZ, W);
-    g.epi.out = dx;
-    g.epi.ld_out = ld_dx;
-    MOE_TRY(launch(g, moe::kNN, L.part, st));
+    data = product(T, K, N, moe::kEpiOut, f32);
+    add_segments(data, f32, DZ, W);
+    data.epi.out = dx;
+    data.epi.ld_out = ld_dx;
   }
   if (dw != nullptr) {
-    moe::DenseArgs g = product(N, K, T, moe::kEpiOut, f32);
-    add_segments(g, f32, DZ, X);
-    g.epi.out = dw;
-    g.epi.ld_out = K;
-    MOE_TRY(launch(g, moe::kTN, L.part, st));
+    weights.g[0] = product(N, K, T, moe::kEpiOut, f32);
+    add_segments(weights.g[0], f32, DZ, X);
+    weights.g[0].epi.out = dw;
+    weights.g[0].epi.ld_out = K;
   }
+  if (dx != nullptr && dw != nullptr) MOE_TRY(moe::launch_dense_gradients(data, weights, 1, L.part, st));
+  else if (dx != nullptr) MOE_TRY(launch(data, moe::kNN, L.part, st));
+  else if (dw != nullptr) MOE_TRY(moe::launch_dense(weights, 1, moe::kTN, L.part, st));
   return MOE_OK;
 }
 
@@ -566,7 +569,6 @@ int moe_ffn_backward(const moe_ffn_cfg* cfg, int64_t T, const void* x, int64_t l
   add_segments(g, f32, DU, WU);
   g.epi.out = dx;
   g.epi.ld_out = ld_dx;
-  MOE_TRY(launch(g, moe::kNN, F.part, st));
   const struct { const Mat &a, &b; int rows, cols; void* out; } grads[3] = {
       {DG, X, I, H, dw_gate}, {DU, X, I, H, dw_up}, {DY, MID, H, I, dw_down}};
   moe::DenseGroup group{};
@@ -576,7 +578,7 @@ int moe_ffn_backward(const moe_ffn_cfg* cfg, int64_t T, const void* x, int64_t l
     group.g[i].epi.out = grads[i].out;
     group.g[i].epi.ld_out = grads[i].cols;
   }
-  MOE_TRY(moe::launch_dense(group, 3, moe::kTN, F.part, st));
+  MOE_TRY(moe::launch_dense_gradients(g, group, 3, F.part, st));
   return MOE_OK;
 }
 
