@@ -295,8 +295,9 @@ int moe_quantize_1x128(const void* x, int64_t rows, int32_t cols, uint8_t* q, fl
  *    no alignment; multiples of 8 elements on 16-byte aligned pointers are
  *    fastest (no operand is then laid out anew).
  *  - T <= 2^24 and sizes <= 131072, else MOE_ERR_SHAPE.
- *  - Workspaces are aligned to 16 bytes (else MOE_ERR_WORKSPACE).  Outputs may
- *    not overlap inputs or each other, but where stated.
+ *  - Workspaces are aligned to 16 bytes (else MOE_ERR_WORKSPACE).  The size
+ *    asked for one T never falls as T grows: it serves every smaller batch too.
+ *  - Outputs may not overlap inputs or each other, but where stated.
  *  - T == 0 returns MOE_OK and writes nothing, gradients included.
  *  - moe_profile_* does not record them.
  */

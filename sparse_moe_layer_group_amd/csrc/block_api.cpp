@@ -196,8 +196,21 @@ void stage_to(moe::DenseEpi& e, const Mat& m, int64_t rows) {
   e.ld_p = m.ld;
   e.plane = rows * m.ld;
 }
-size_t part_bytes(int64_t M, int N, int64_t K, bool f32, int pairs = 1, int dual = 0, int count = 1) {
-  return moe::dense_part_bytes(M, N, K, pairs * (f32 ? kPairs : 1), dual, count);
+// Which batches a workspace is laid out for.  A call asks for its own; a query
+// for its own and every smaller one, so that a workspace made once serves them
+// all: the sums of split contractions, alone in this, take more room for some
+// smaller batches, which have fewer tiles and more splits.
+enum Batches { kThis, kUpTo };
+// room for split sums of a product with T rows, and of one that contracts over T
+size_t rows_part(Batches b, int64_t T, int N, int64_t K, bool f32, int pairs = 1, int dual = 0) {
+  const int segments = pairs * (f32 ? kPairs : 1);
+  return b == kThis ? moe::dense_part_bytes(T, N, K, segments, dual, 1)
+                    : moe::dense_part_most(T, N, K, segments, dual, 1);
+}
+size_t deep_part(Batches b, int64_t M, int N, int64_t T, bool f32, int count = 1) {
+  const int segments = f32 ? kPairs : 1;
+  return b == kThis ? moe::dense_part_bytes(M, N, T, segments, 0, count)
+                    : moe::dense_part_most_deep(M, N, T, segments, count);
 }
 hipError_t launch(const moe::DenseArgs& g, int layout, float* part, hipStream_t st) {
   moe::DenseGroup group{};
@@ -228,20 +241,20 @@ struct LinearWork {
   float *part, *sums;
   size_t bytes;
 };
-LinearWork linear_carve(const moe_linear_cfg& c, int64_t T, bool back, void* ws, const void* x, int64_t ld_x,
-                        const void* w, const void* dy, int64_t ld_dy) {
+LinearWork linear_carve(const moe_linear_cfg& c, Batches b, int64_t T, bool back, void* ws, const void* x,
+                        int64_t ld_x, const void* w, const void* dy, int64_t ld_dy) {
   const bool f32 = c.dtype == MOE_F32;
   const int K = c.in_dim, N = c.out_dim;
   Carver v{static_cast<char*>(ws)};
   LinearWork L{};
   L.x = source(v, f32, x, ld_x, T, K);
   L.w = source(v, f32, w, K, N, K);
-  size_t part = part_bytes(T, N, K, f32);
+  size_t part = rows_part(b, T, N, K, f32);
   if (back) {
     if (c.act == MOE_ACT_NONE) L.dy = source(v, f32, dy, ld_dy, T, N);
     else L.dz = v.take<bf16_t>(planes_bytes(f32, T, N));
-    part = std::max(part, part_bytes(T, K, N, f32));
-    part = std::max(part, part_bytes(N, K, T, f32));
+    part = std::max(part, rows_part(b, T, K, N, f32));
+    part = std::max(part, deep_part(b, N, K, T, f32));
     L.sums = v.take<float>(moe::dense_colsum_bytes(T, N));
   }
   L.part = v.take<float>(part);
@@ -266,8 +279,8 @@ struct FfnWork {
   float* part;
   size_t bytes;
 };
-FfnWork ffn_carve(const moe_ffn_cfg& c, int64_t T, bool back, void* ws, const void* x, int64_t ld_x, const void* wg,
-                  const void* wu, const void* wd, const void* dy, int64_t ld_dy) {
+FfnWork ffn_carve(const moe_ffn_cfg& c, Batches b, int64_t T, bool back, void* ws, const void* x, int64_t ld_x,
+                  const void* wg, const void* wu, const void* wd, const void* dy, int64_t ld_dy) {
   const bool f32 = c.dtype == MOE_F32;
   const int H = c.hidden, I = c.inter;
   Carver v{static_cast<char*>(ws)};
@@ -277,19 +290,19 @@ FfnWork ffn_carve(const moe_ffn_cfg& c, int64_t T, bool back, void* ws, const vo
   F.wu = source(v, f32, wu, H, I, H);
   F.wd = source(v, f32, wd, I, H, I);
   F.mid = v.take<bf16_t>(planes_bytes(f32, T, I));
-  size_t part = part_bytes(T, I, H, f32, 1, 1);
+  size_t part = rows_part(b, T, I, H, f32, 1, 1);
   if (back) {
     F.dy = source(v, f32, dy, ld_dy, T, H);
     F.dg = v.take<bf16_t>(planes_bytes(f32, T, I));
     F.du = v.take<bf16_t>(planes_bytes(f32, T, I));
     F.g = v.take<float>(size_t(T) * size_t(padded(I)) * sizeof(float));
     F.u = v.take<float>(size_t(T) * size_t(padded(I)) * sizeof(float));
-    part = std::max(part, part_bytes(T, I, H, f32));
-    part = std::max(part, part_bytes(T, H, I, f32, 2));
-    part = std::max(part, part_bytes(I, H, T, f32, 1, 0, 3));
-    part = std::max(part, part_bytes(H, I, T, f32, 1, 0, 3));
+    part = std::max(part, rows_part(b, T, I, H, f32));
+    part = std::max(part, rows_part(b, T, H, I, f32, 2));
+    part = std::max(part, deep_part(b, I, H, T, f32, 3));
+    part = std::max(part, deep_part(b, H, I, T, f32, 3));
   } else {
-    part = std::max(part, part_bytes(T, H, I, f32));
+    part = std::max(part, rows_part(b, T, H, I, f32));
   }
   F.part = v.take<float>(part);
   F.bytes = v.used;
@@ -371,7 +384,7 @@ int moe_norm_backward(const moe_norm_cfg* cfg, int64_t T, const void* residual, 
 
 size_t moe_linear_workspace_bytes(const moe_linear_cfg* cfg, int64_t T) {
   if (validate(cfg, T) != MOE_OK || T == 0) return 0;
-  return linear_carve(*cfg, T, false, nullptr, nullptr, 0, nullptr, nullptr, 0).bytes;
+  return linear_carve(*cfg, kUpTo, T, false, nullptr, nullptr, 0, nullptr, nullptr, 0).bytes;
 }
 
 int moe_linear_forward(const moe_linear_cfg* cfg, int64_t T, const void* x, int64_t ld_x, const void* w,
@@ -382,7 +395,7 @@ int moe_linear_forward(const moe_linear_cfg* cfg, int64_t T, const void* x, int6
   if (x == nullptr || w == nullptr || y == nullptr) return MOE_ERR_NULL;
   const int K = cfg->in_dim, N = cfg->out_dim;
   if (bad_ld(x, ld_x, K) || bad_ld(residual, ld_residual, N) || bad_ld(y, ld_y, N)) return MOE_ERR_SHAPE;
-  const LinearWork L = linear_carve(*cfg, T, false, ws, x, ld_x, w, nullptr, 0);
+  const LinearWork L = linear_carve(*cfg, kThis, T, false, ws, x, ld_x, w, nullptr, 0);
   if (bad_ws(ws, ws_bytes, L.bytes)) return MOE_ERR_WORKSPACE;
   if ((rc = check_device()) != MOE_OK) return rc;
   const bool f32 = cfg->dtype == MOE_F32;
@@ -410,7 +423,7 @@ int moe_linear_forward(const moe_linear_cfg* cfg, int64_t T, const void* x, int6
 
 size_t moe_linear_backward_workspace_bytes(const moe_linear_cfg* cfg, int64_t T) {
   if (validate(cfg, T) != MOE_OK || T == 0) return 0;
-  return linear_carve(*cfg, T, true, nullptr, nullptr, 0, nullptr, nullptr, 0).bytes;
+  return linear_carve(*cfg, kUpTo, T, true, nullptr, nullptr, 0, nullptr, nullptr, 0).bytes;
 }
 
 int moe_linear_backward(const moe_linear_cfg* cfg, int64_t T, const void* x, int64_t ld_x, const void* w,
@@ -421,7 +434,7 @@ int moe_linear_backward(const moe_linear_cfg* cfg, int64_t T, const void* x, int
   if (x == nullptr || w == nullptr || dy == nullptr) return MOE_ERR_NULL;
   const int K = cfg->in_dim, N = cfg->out_dim;
   if (bad_ld(x, ld_x, K) || bad_ld(dy, ld_dy, N) || bad_ld(dx, ld_dx, K)) return MOE_ERR_SHAPE;
-  const LinearWork L = linear_carve(*cfg, T, true, ws, x, ld_x, w, dy, ld_dy);
+  const LinearWork L = linear_carve(*cfg, kThis, T, true, ws, x, ld_x, w, dy, ld_dy);
   if (bad_ws(ws, ws_bytes, L.bytes)) return MOE_ERR_WORKSPACE;
   if (dx == nullptr && dw == nullptr && dbias == nullptr) return MOE_OK;
   if ((rc = check_device()) != MOE_OK) return rc;
@@ -474,7 +487,7 @@ int moe_linear_backward(const moe_linear_cfg* cfg, int64_t T, const void* x, int
 
 size_t moe_ffn_workspace_bytes(const moe_ffn_cfg* cfg, int64_t T) {
   if (validate(cfg, T) != MOE_OK || T == 0) return 0;
-  return ffn_carve(*cfg, T, false, nullptr, nullptr, 0, nullptr, nullptr, nullptr, nullptr, 0).bytes;
+  return ffn_carve(*cfg, kUpTo, T, false, nullptr, nullptr, 0, nullptr, nullptr, nullptr, nullptr, 0).bytes;
 }
 
 int moe_ffn_forward(const moe_ffn_cfg* cfg, int64_t T, const void* x, int64_t ld_x, const void* w_gate,
@@ -485,7 +498,7 @@ int moe_ffn_forward(const moe_ffn_cfg* cfg, int64_t T, const void* x, int64_t ld
   if (x == nullptr || w_gate == nullptr || w_up == nullptr || w_down == nullptr || y == nullptr) return MOE_ERR_NULL;
   const int H = cfg->hidden, I = cfg->inter;
   if (bad_ld(x, ld_x, H) || bad_ld(residual, ld_residual, H) || bad_ld(y, ld_y, H)) return MOE_ERR_SHAPE;
-  const FfnWork F = ffn_carve(*cfg, T, false, ws, x, ld_x, w_gate, w_up, w_down, nullptr, 0);
+  const FfnWork F = ffn_carve(*cfg, kThis, T, false, ws, x, ld_x, w_gate, w_up, w_down, nullptr, 0);
   if (bad_ws(ws, ws_bytes, F.bytes)) return MOE_ERR_WORKSPACE;
   if ((rc = check_device()) != MOE_OK) return rc;
   const bool f32 = cfg->dtype == MOE_F32;
@@ -521,7 +534,7 @@ int moe_ffn_forward(const moe_ffn_cfg* cfg, int64_t T, const void* x, int64_t ld
 
 size_t moe_ffn_backward_workspace_bytes(const moe_ffn_cfg* cfg, int64_t T) {
   if (validate(cfg, T) != MOE_OK || T == 0) return 0;
-  return ffn_carve(*cfg, T, true, nullptr, nullptr, 0, nullptr, nullptr, nullptr, nullptr, 0).bytes;
+  return ffn_carve(*cfg, kUpTo, T, true, nullptr, nullptr, 0, nullptr, nullptr, nullptr, nullptr, 0).bytes;
 }
 
 int moe_ffn_backward(const moe_ffn_cfg* cfg, int64_t T, const void* x, int64_t ld_x, const void* w_gate,
@@ -534,7 +547,7 @@ int moe_ffn_backward(const moe_ffn_cfg* cfg, int64_t T, const void* x, int64_t l
     return MOE_ERR_NULL;
   const int H = cfg->hidden, I = cfg->inter;
   if (bad_ld(x, ld_x, H) || bad_ld(dy, ld_dy, H) || bad_ld(dx, ld_dx, H)) return MOE_ERR_SHAPE;
-  const FfnWork F = ffn_carve(*cfg, T, true, ws, x, ld_x, w_gate, w_up, w_down, dy, ld_dy);
+  const FfnWork F = ffn_carve(*cfg, kThis, T, true, ws, x, ld_x, w_gate, w_up, w_down, dy, ld_dy);
   if (bad_ws(ws, ws_bytes, F.bytes)) return MOE_ERR_WORKSPACE;
   if ((rc = check_device()) != MOE_OK) return rc;
   const bool f32 = cfg->dtype == MOE_F32;

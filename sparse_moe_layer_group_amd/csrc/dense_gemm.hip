@@ -536,22 +536,26 @@ constexpr double kJoinOnce = 5.5, kJoinBytesPerUs = 4.5e6;  // of a split contra
 // narrow: the 64 x 32 tile is there, for forward products of few tokens, whose
 // weights should pass through as many CUs as there are (50 tokens by 7168 rows
 // of 2048: 11.3 us against 13.5 by 64 x 64 and as much by a split).
+// M counts in whole 64 rows, so that one plan holds for each 64 (dense_part_most).
+constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+constexpr int kSplitGroups = 1024;  // a split leaves at most so many workgroups
 bool narrow(int layout, int mode) { return layout == kNT && mode == kEpiOut; }
 DensePlan dense_plan(int64_t M, int N, int64_t K, int segments, int dual, int count, bool narrow) {
-  const int64_t steps = (K + BK - 1) / BK * segments;
+  const int64_t steps = (K + BK - 1) / BK * segments, rows = (M + 63) & ~int64_t(63);
   DensePlan best{};
   double least = 0;
   for (const TileCost& c : kTileCosts) {
     if (c.tile == 32 && !narrow) break;
     const int64_t tiles = tiles_of(M, N, dual, c.tile) * count;
-    for (int split : {1, 2, 3, 4, 6, 8, 12, 16}) {
-      if (split > 1 && (steps < 4 * split || tiles * split > 1024)) break;
+    for (int split : kSplits) {
+      if (split > 1 && (steps < 4 * split || tiles * split > kSplitGroups)) break;
       const int64_t per = (steps + split - 1) / split, used = (steps + per - 1) / per;
       const int64_t groups = tiles * used, slots = int64_t(256) * c.per_cu;
       const int64_t rest = groups % slots;  // after the full turns of the chip
       double t = double(groups / slots) * (double(per) * c.step[c.per_cu - 1] + c.once);
       if (rest > 0) t += double(per) * c.step[rest > 256 ? 1 : 0] + c.once;
-      if (used > 1) t += kJoinOnce + 8.0 * double(used) * double(count) * double(M) * N * (dual ? 2 : 1) / kJoinBytesPerUs;
+      if (used > 1)
+        t += kJoinOnce + 8.0 * double(used) * double(count) * double(rows) * N * (dual ? 2 : 1) / kJoinBytesPerUs;
       if (best.tile == 0 || t < least) {
         least = t;
         best = DensePlan{c.tile, int(used), int(per)};
@@ -623,6 +627,39 @@ size_t dense_part_bytes(int64_t M, int N, int64_t K, int segments, int dual, int
   for (bool thin : {false, true})
     floats = std::max(floats, part_floats(dense_plan(M, N, K, segments, dual, count, thin && !dual), M, N, dual));
   return size_t(count) * size_t(floats) * sizeof(float);
+}
+
+// The most that dense_part_bytes gives for any M from 1 to this one: the plan
+// is the same for 64 rows at a time, and the last of them take the most.
+size_t dense_part_most(int64_t M, int N, int64_t K, int segments, int dual, int count) {
+  size_t most = 0;
+  if ((K + BK - 1) / BK * segments < 4 * kSplits[1]) return 0;
+  for (int64_t m = 64;; m += 64) {
+    const int64_t at = std::min(m, M);
+    if (tiles_of(at, N, dual, kTileCosts[0].tile) * count * kSplits[1] > kSplitGroups) return most;  // nor further on
+    most = std::max(most, dense_part_bytes(at, N, K, segments, dual, count));
+    if (at == M) return most;
+  }
+}
+
+// At least what dense_part_bytes gives for any K up to this one.  A split into u
+// parts takes per >= steps / u steps a part, so where the turns of the chip that
+// its groups take cost no less, divided by u, than the whole product's, the
+// whole product (no join) always costs less.
+size_t dense_part_most_deep(int64_t M, int N, int64_t K, int segments, int count) {
+  const int64_t steps = (K + BK - 1) / BK * segments;
+  int most = 1;
+  for (const TileCost& c : kTileCosts) {
+    const int64_t tiles = tiles_of(M, N, 0, c.tile) * count, slots = int64_t(256) * c.per_cu;
+    if (c.tile == 32) break;  // forward products only
+    auto turns = [&](int u) {  // microseconds that a step of every group takes
+      const int64_t rest = tiles * u % slots;
+      return double(tiles * u / slots) * c.step[c.per_cu - 1] + (rest == 0 ? 0.0 : c.step[rest > 256 ? 1 : 0]);
+    };
+    for (int u = kSplits[7]; u > most; --u)
+      if (steps >= 4 * u && tiles * u <= kSplitGroups && turns(u) < u * turns(1)) most = u;
+  }
+  return size_t(count) * size_t(part_floats(DensePlan{0, most, 0}, M, N, 0)) * sizeof(float);
 }
 
 namespace {
