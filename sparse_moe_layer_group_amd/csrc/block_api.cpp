@@ -129,8 +129,9 @@ Mat planes_at(bool f32, bf16_t* p, int64_t rows, int64_t cols) {
 }
 
 // A user's matrix: as it is where the products can read it, else laid out
-// anew at `room` (float32: split into planes).  The room is part of every
-// workspace, whose size goes by the configuration alone.
+// anew at `room` (float32: split into planes).  The room is part of the
+// workspace of every call that goes to the tiles, as its size goes by the
+// configuration alone.
 struct Source {
   const void* p;
   int64_t ld, rows;
@@ -247,6 +248,11 @@ LinearWork linear_carve(const moe_linear_cfg& c, Batches b, int64_t T, bool back
   const int K = c.in_dim, N = c.out_dim;
   Carver v{static_cast<char*>(ws)};
   LinearWork L{};
+  if (!back && streams(T, f32)) {  // nothing but a size that is not 0, which a query has for what is invalid
+    v.take<char>(1);
+    L.bytes = v.used;
+    return L;
+  }
   L.x = source(v, f32, x, ld_x, T, K);
   L.w = source(v, f32, w, K, N, K);
   size_t part = rows_part(b, T, N, K, f32);
@@ -274,7 +280,7 @@ int validate(const moe_ffn_cfg* c, int64_t T) {
 
 struct FfnWork {
   Source x, wg, wu, wd, dy;
-  bf16_t *mid, *dg, *du;  // staged operands [T][inter]
+  bf16_t *mid, *dg, *du;  // staged operands [T][inter] (few tokens: mid of the call's type)
   float *g, *u;           // the projections, float32 (backward)
   float* part;
   size_t bytes;
@@ -285,6 +291,11 @@ FfnWork ffn_carve(const moe_ffn_cfg& c, Batches b, int64_t T, bool back, void* w
   const int H = c.hidden, I = c.inter;
   Carver v{static_cast<char*>(ws)};
   FfnWork F{};
+  if (!back && streams(T, f32)) {  // packed rows of the type
+    F.mid = v.take<bf16_t>(size_t(T) * size_t(I) * (f32 ? sizeof(float) : sizeof(bf16_t)));
+    F.bytes = v.used;
+    return F;
+  }
   F.x = source(v, f32, x, ld_x, T, H);
   F.wg = source(v, f32, wg, H, I, H);
   F.wu = source(v, f32, wu, H, I, H);

@@ -52,3 +52,14 @@ def test_sizes_of_large_batches_never_fall(dtype):
 def test_norm_sizes_never_fall(dtype, kind, gate_rows):
     for H in (72, 1000, 7168, 16384):
         _never_falls(moe.norm_backward_workspace_bytes, moe.make_norm_cfg(H, dtype, kind, gate_rows), range(3000))
+
+
+@pytest.mark.parametrize("dtype,most", [("bf16", 16), ("f32", 64)])
+@pytest.mark.parametrize("K,N", [(7168, 7168), (1001, 777)])
+def test_few_tokens_need_no_copies_of_the_weights(dtype, most, K, N):
+    # up to `most` tokens the weights are read where they lie; a block keeps its middle alone
+    size = 2 if dtype == "bf16" else 4
+    for T in (1, most):
+        assert 0 < moe.linear_workspace_bytes(moe.make_linear_cfg(K, N, "gelu", dtype), T) <= 256
+        assert 0 < moe.ffn_workspace_bytes(moe.make_ffn_cfg(K, N, "gelu", dtype), T) <= T * N * size + 256
+    assert moe.linear_workspace_bytes(moe.make_linear_cfg(K, N, "gelu", dtype), most + 1) > K * N * 2
