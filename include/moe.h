@@ -299,6 +299,8 @@ int moe_quantize_1x128(const void* x, int64_t rows, int32_t cols, uint8_t* q, fl
  *    asked for one T never falls as T grows: it serves every smaller batch too.
  *  - Outputs may not overlap inputs or each other, but where stated.
  *  - T == 0 returns MOE_OK and writes nothing, gradients included.
+ *  - A NaN comes out where float32 arithmetic has one, through every activation
+ *    and its slope.
  *  - moe_profile_* does not record them.
  */
 

@@ -11,8 +11,9 @@ namespace moe {
 // codes of enum moe_act
 constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3;
 
-MOE_DEV float relu_value(float z) { return fmaxf(z, 0.f); }
-MOE_DEV float relu_slope(float z) { return z > 0.f ? 1.f : 0.f; }
+// (NaN stays NaN, in the slope too, as in the others: a maximum would hide it)
+MOE_DEV float relu_value(float z) { return z < 0.f ? 0.f : z; }
+MOE_DEV float relu_slope(float z) { return z > 0.f ? 1.f : z <= 0.f ? 0.f : z; }
 MOE_DEV float silu_slope(float z) {
   const float s = sigmoidf(z);
   return s * (1.0f + z * (1.0f - s));
