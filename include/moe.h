@@ -299,8 +299,9 @@ int moe_quantize_1x128(const void* x, int64_t rows, int32_t cols, uint8_t* q, fl
  *    asked for one T never falls as T grows: it serves every smaller batch too.
  *  - Outputs may not overlap inputs or each other, but where stated.
  *  - T == 0 returns MOE_OK and writes nothing, gradients included.
- *  - A NaN comes out where float32 arithmetic has one, through every activation
- *    and its slope.
+ *  - NaN and infinity in the operands of products come out where float32
+ *    arithmetic has them, NaN through every activation and its slope too.  (F32:
+ *    two infinities that meet in one product of a sum give NaN.)
  *  - moe_profile_* does not record them.
  */
 

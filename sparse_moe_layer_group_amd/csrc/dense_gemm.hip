@@ -121,20 +121,8 @@ MOE_DEV void store_planes(const DenseEpi& e, bf16_t* p, int64_t offset, const fl
     *reinterpret_cast<u32x4*>(at) = pack8(v);
     return;
   }
-  float r[8];
   u32x4 o[3];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = v[i];
-#pragma unroll
-  for (int s = 0; s < 3; ++s)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // truncation: what is left is exact
-      const uint32_t lo = __float_as_uint(r[2 * i]) & 0xffff0000u, hi = __float_as_uint(r[2 * i + 1]) & 0xffff0000u;
-      o[s][i] = (lo >> 16) | hi;
-      r[2 * i] -= __uint_as_float(lo);
-      r[2 * i + 1] -= __uint_as_float(hi);
-    }
+  split_any8(v, o);
 #pragma unroll
   for (int s = 0; s < 3; ++s) *reinterpret_cast<u32x4*>(at + s * e.plane) = o[s];
 }
@@ -280,12 +268,10 @@ MOE_DEV void store_plane1(const DenseEpi& e, bf16_t* p, int64_t offset, float v)
     p[offset] = f32_to_bf16(v);
     return;
   }
+  bf16_t o[3];
+  split1(v, o);
 #pragma unroll
-  for (int s = 0; s < 3; ++s) {
-    const uint32_t hi = __float_as_uint(v) & 0xffff0000u;
-    p[offset + s * e.plane] = bf16_t(hi >> 16);
-    v -= __uint_as_float(hi);
-  }
+  for (int s = 0; s < 3; ++s) p[offset + s * e.plane] = o[s];
 }
 MOE_DEV float load1(const DenseEpi& e, const void* p, int64_t at) {
   return e.f32 ? static_cast<const float*>(p)[at] : bf16_to_f32(static_cast<const bf16_t*>(p)[at]);

@@ -36,7 +36,7 @@ template <> struct Part8<bf16_t> {
   MOE_DEV void load(const bf16_t* p, int k, int K, bool inside) {
     raw = inside ? reinterpret_cast<const u32x4_at2*>(p + k)->v : load8_raw<false>(p, k, K);
   }
-  MOE_DEV void parts(bf16x8 (&o)[1]) const { o[0] = __builtin_bit_cast(bf16x8, raw); }
+  template <bool> MOE_DEV void parts(bf16x8 (&o)[1]) const { o[0] = __builtin_bit_cast(bf16x8, raw); }
 };
 template <> struct Part8<float> {
   static constexpr int N = 3;
@@ -45,22 +45,11 @@ template <> struct Part8<float> {
     if (inside) load8<true>(p, k, k + 8, v);
     else load8<false>(p, k, K, v);
   }
-  MOE_DEV void parts(bf16x8 (&o)[3]) const {
-    float r[8];
+  template <bool ANY> MOE_DEV void parts(bf16x8 (&o)[3]) const {
+    u32x4 w[3];
+    split8<ANY>(v, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = v[i];
-#pragma unroll
-    for (int s = 0; s < 3; ++s) {
-      u32x4 w;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = __float_as_uint(r[2 * i]) & 0xffff0000u, hi = __float_as_uint(r[2 * i + 1]) & 0xffff0000u;
-        w[i] = (lo >> 16) | hi;
-        r[2 * i] -= __uint_as_float(lo);
-        r[2 * i + 1] -= __uint_as_float(hi);
-      }
-      o[s] = __builtin_bit_cast(bf16x8, w);
-    }
+    for (int s = 0; s < 3; ++s) o[s] = __builtin_bit_cast(bf16x8, w[s]);
   }
 };
 
@@ -127,11 +116,39 @@ template <class S> __global__ __launch_bounds__(64 * kWaves) void dense_stream_k
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
       bf16x8 a[Part8<TE>::N], b[Part8<TE>::N];
-      wc[s].parts(a);
+      wc[s].template parts<false>(a);
 #pragma unroll
       for (int i = 0; i < TT; ++i) {
-        xc[i][s].parts(b);
+        xc[i][s].template parts<false>(b);
         acc[i] = mfma_parts(a, b, acc[i]);
+      }
+    }
+  }
+  // An infinity whose parts were taken as another value's has left a NaN in the
+  // sums, and so may others: such a wave's share once more, with split8<true>.
+  // (Asking for infinities before each turn holds all of its values at once and
+  // spilled 32 registers from 33 tokens on.)
+  bool again = false;
+#pragma unroll
+  for (int i = 0; i < TT; ++i)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) again = again || acc[i][v] != acc[i][v];
+  if (Part8<TE>::N > 1 && __builtin_amdgcn_ballot_w64(again) != 0) {
+#pragma unroll
+    for (int i = 0; i < TT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (k0 = wave * kTurn; k0 < g.K; k0 += kWaves * kTurn) {
+#pragma unroll 1
+      for (int k = k0; k < k0 + kTurn; k += 32) {
+        Part8<TE> v;
+        bf16x8 a[Part8<TE>::N], b[Part8<TE>::N];
+        v.load(w, k + kq, g.K, k0 + kTurn <= g.K);
+        v.template parts<true>(a);
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+          v.load(x[i], k + kq, g.K, k0 + kTurn <= g.K);
+          v.template parts<true>(b);
+          acc[i] = mfma_parts(a, b, acc[i]);
+        }
       }
     }
   }
