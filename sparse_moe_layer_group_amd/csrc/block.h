@@ -150,34 +150,34 @@ template <bool WHOLE> MOE_DEV void store8(bf16_t* row, int c, int n, const float
 
 // ---------------------------------------------------------------- float32 as three bfloat16 parts
 
-// v = part 0 + part 1 + part 2, exactly: each part is what 8 bits of the rest
-// hold, by truncation, so that what is left is exact.  A value that is not
-// finite is part 2 alone, its others are 0: of the products that stand for
-// v w, part 2 takes part in one, with w's part 0, and an infinity then meets
-// neither a 0 nor a part of the other sign.  (Two infinities at the same place
-// of a contraction give NaN.)
+// v = part 0 + part 1 + part 2, exactly: each part is what is left, rounded to
+// nearest, so part 1 is up to 2^-8 of v and part 2 up to 2^-17, of either sign,
+// and the pairs of parts that a product leaves out (below 2^-24 of it) do not
+// add up over a sum as truncated parts' did, which were four times as large.
+// Where part 0 would round up past the largest bfloat16 it is that one.  A value
+// that is not finite is part 2 alone, its others are 0: of the products that
+// stand for v w, part 2 takes part in one, with w's part 0, and an infinity then
+// meets neither a 0 nor a part of the other sign.  (Two infinities at the same
+// place of a contraction give NaN.)
 MOE_DEV bool finite(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
-// (a NaN may have its mark in the bits that truncation drops)
-MOE_DEV float marked(float v) { return v != v ? __builtin_nanf("") : v; }
+constexpr float kMostBf16 = 0x1.fep127f;
+MOE_DEV float first_of(float v) { return __builtin_amdgcn_fmed3f(v, -kMostBf16, kMostBf16); }
 
-// ANY: whatever the values; else an infinity's parts are NaN but for the first
+// ANY: whatever the values; else the parts of one above kMostBf16 may be
+// infinite and NaN
 template <bool ANY> MOE_DEV void split8(const float (&v)[8], u32x4 (&o)[3]) {
   float r[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) r[i] = !ANY || finite(v[i]) ? v[i] : 0.f;
 #pragma unroll
   for (int s = 0; s < 3; ++s) {
+    float t[8], p[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (ANY && s == 2) {
-        r[2 * i] = finite(v[2 * i]) ? r[2 * i] : marked(v[2 * i]);
-        r[2 * i + 1] = finite(v[2 * i + 1]) ? r[2 * i + 1] : marked(v[2 * i + 1]);
-      }
-      const uint32_t lo = __float_as_uint(r[2 * i]) & 0xffff0000u, hi = __float_as_uint(r[2 * i + 1]) & 0xffff0000u;
-      o[s][i] = (lo >> 16) | hi;
-      r[2 * i] -= __uint_as_float(lo);
-      r[2 * i + 1] -= __uint_as_float(hi);
-    }
+    for (int i = 0; i < 8; ++i) t[i] = !ANY || s == 1 ? r[i] : s == 0 ? first_of(r[i]) : finite(v[i]) ? r[i] : v[i];
+    o[s] = pack8(t);
+    unpack8(o[s], p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] -= p[i];
   }
 }
 MOE_DEV void split_any8(const float (&v)[8], u32x4 (&o)[3]) {
@@ -185,17 +185,15 @@ MOE_DEV void split_any8(const float (&v)[8], u32x4 (&o)[3]) {
 #pragma unroll
   for (int i = 0; i < 8; i += 2)
     asm("v_max3_f32 %0, %1, |%2|, |%3|" : "=v"(most) : "v"(most), "v"(v[i]), "v"(v[i + 1]));
-  if (__builtin_expect(__builtin_amdgcn_ballot_w64(most == __builtin_inff()) != 0, 0)) split8<true>(v, o);
+  if (__builtin_expect(__builtin_amdgcn_ballot_w64(most > kMostBf16) != 0, 0)) split8<true>(v, o);
   else split8<false>(v, o);
 }
 MOE_DEV void split1(float v, bf16_t (&o)[3]) {
   float r = finite(v) ? v : 0.f;
 #pragma unroll
   for (int s = 0; s < 3; ++s) {
-    if (s == 2) r = finite(v) ? r : marked(v);
-    const uint32_t hi = __float_as_uint(r) & 0xffff0000u;
-    o[s] = bf16_t(hi >> 16);
-    r -= __uint_as_float(hi);
+    o[s] = f32_to_bf16(s == 0 ? first_of(r) : s == 2 && !finite(v) ? v : r);
+    r -= bf16_to_f32(o[s]);
   }
 }
 

@@ -164,7 +164,8 @@ struct Operands {
 };
 
 // Segments of A B over the planes, smallest terms first.  Of float32's nine
-// pairs, mid lo, lo mid and lo lo are below 2^-24 of the product and left out.
+// pairs, mid lo and lo mid are up to 2^-25 of the product each, lo lo 2^-34: left
+// out.
 constexpr int kPairs = 6;
 constexpr int kPairA[kPairs] = {2, 0, 1, 1, 0, 0}, kPairB[kPairs] = {0, 2, 1, 0, 1, 0};
 

@@ -7,8 +7,8 @@
 // dimension, the tokens).  A dual product takes two B matrices at once (the
 // gate and up projections), so their elementwise product is formed from the
 // two accumulators.  float32 operands come as three bfloat16 planes, hi + mid
-// + lo exactly, and a product as six segments of the contraction (all pairs
-// whose weight is 2^-16 or more; the rest is below float32's own rounding).
+// + lo exactly, and a product as six segments of the contraction (all pairs but
+// those below 2^-24 of the product, which is float32's own rounding).
 //
 // Bound by the matrix cores, and at that by power: a loop of nothing but MFMAs
 // sustains 2.0 PFLOP/s with 16x16x32 blocks and 1.8 with 32x32x16 on values of

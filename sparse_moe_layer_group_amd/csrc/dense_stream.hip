@@ -124,8 +124,8 @@ template <class S> __global__ __launch_bounds__(64 * kWaves) void dense_stream_k
       }
     }
   }
-  // An infinity whose parts were taken as another value's has left a NaN in the
-  // sums, and so may others: such a wave's share once more, with split8<true>.
+  // A value that needs split8<true> and had split8<false> has left a NaN in the
+  // sums, and so may others: such a wave's share once more.
   // (Asking for infinities before each turn holds all of its values at once and
   // spilled 32 registers from 33 tokens on.)
   bool again = false;
