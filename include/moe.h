@@ -405,7 +405,8 @@ int moe_linear_forward(const moe_linear_cfg* cfg, int64_t T, const void* x, int6
 /*
  * Gradients of <dy, y> (the residual's is dy itself).  dx [T][in_dim],
  * dw [out_dim][in_dim], dbias [out_dim]; each may be NULL (not wanted).  With
- * an activation the sums before it are recomputed from x, w and bias.
+ * an activation the sums before it are recomputed from x, w and bias; dbias
+ * sums the gradient there in float32, before it is rounded as an operand.
  */
 size_t moe_linear_backward_workspace_bytes(const moe_linear_cfg* cfg, int64_t T);
 int moe_linear_backward(const moe_linear_cfg* cfg, int64_t T, const void* x, int64_t ld_x,

@@ -244,6 +244,8 @@ struct DenseEpi {
   bf16_t *p0, *p1, *p2;     // staged operands: [f32 ? 3 : 1][M][ld_p], columns N .. ld_p up to 8 written as 0
   int64_t plane, ld_p;      // elements between planes, and rows
   float *g, *u;             // [M][ld_p]
+  float* sums;              // kEpiActBack: [row tiles x 2][N], sums over the rows, or NULL (not wanted).  A split
+                            // contraction leaves the results themselves in its first part instead.
 };
 
 // out[m][n] = sum over segments and k of A[m][k] B[n][k], each operand given
@@ -305,9 +307,12 @@ constexpr int kMaxPacks = 5;
 struct PackJobs { PackJob j[kMaxPacks]; };
 hipError_t launch_dense_pack(const PackJobs& jobs, int count, bool f32, hipStream_t st);
 
-// out[n] = sum over rows of src[r][n]; planes as above (n_planes 1 or 3) or, n_planes 0, float32
-size_t dense_colsum_bytes(int64_t rows, int cols);
-hipError_t launch_dense_colsum(const void* src, int64_t ld, int n_planes, int64_t plane, int64_t rows, int cols,
-                               void* out, bool f32, float* part, hipStream_t st);
+// Sums over rows: out[n] = sum over r of src[r][n], src bfloat16 or float32 (src_f32);
+// and a product with kEpiActBack with those of its results, unrounded, as dbias
+// (NULL: not wanted).  sums: dense_sums_bytes of room.
+size_t dense_sums_bytes(int64_t rows, int cols);
+hipError_t launch_dense_colsum(const void* src, bool src_f32, int64_t ld, int64_t rows, int cols, void* out, bool f32,
+                               float* sums, hipStream_t st);
+hipError_t launch_dense_act_back(const DenseArgs& g, void* dbias, float* sums, float* part, hipStream_t st);
 
 }  // namespace moe

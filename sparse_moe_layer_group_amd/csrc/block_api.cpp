@@ -262,7 +262,7 @@ LinearWork linear_carve(const moe_linear_cfg& c, Batches b, int64_t T, bool back
     else L.dz = v.take<bf16_t>(planes_bytes(f32, T, N));
     part = std::max(part, rows_part(b, T, K, N, f32));
     part = std::max(part, deep_part(b, N, K, T, f32));
-    L.sums = v.take<float>(moe::dense_colsum_bytes(T, N));
+    L.sums = v.take<float>(moe::dense_sums_bytes(T, N));
   }
   L.part = v.take<float>(part);
   L.bytes = v.used;
@@ -460,7 +460,7 @@ int moe_linear_backward(const moe_linear_cfg* cfg, int64_t T, const void* x, int
   MOE_TRY(ops.lay_out(st));
   if (plain) {
     if (dbias != nullptr)
-      MOE_TRY(moe::launch_dense_colsum(dy, ld_dy, f32 ? 0 : 1, 0, T, N, dbias, f32, L.sums, st));
+      MOE_TRY(moe::launch_dense_colsum(dy, f32, ld_dy, T, N, dbias, f32, L.sums, st));
   } else {
     DZ = planes_at(f32, L.dz, T, N);
     moe::DenseArgs g = product(T, N, K, moe::kEpiActBack, f32);
@@ -471,9 +471,7 @@ int moe_linear_backward(const moe_linear_cfg* cfg, int64_t T, const void* x, int
     g.epi.ld_dy = ld_dy;
     g.epi.p0 = L.dz;
     stage_to(g.epi, DZ, T);
-    MOE_TRY(launch(g, moe::kNT, L.part, st));
-    if (dbias != nullptr)
-      MOE_TRY(moe::launch_dense_colsum(L.dz, DZ.ld, f32 ? 3 : 1, T * DZ.ld, T, N, dbias, f32, L.sums, st));
+    MOE_TRY(moe::launch_dense_act_back(g, dbias, L.sums, L.part, st));
   }
   moe::DenseArgs data{};
   moe::DenseGroup weights{};

@@ -163,10 +163,12 @@ template <int MODE, bool INSIDE> MOE_DEV void load_bias(const DenseEpi& e, int n
 // e.residual is there.  (Asked at both its load and its use, it leaves the
 // compiler a path with loads that nothing waited for, and it then waits for all
 // memory operations, the stores too, before the next rows.)  early: the rows of
-// the residual or upstream gradient, where they were loaded before.
+// the residual or upstream gradient, where they were loaded before.  total:
+// kEpiActBack's results are added to it, as they are before they are rounded,
+// and left in v.
 template <int MODE, bool INSIDE, bool RESIDUAL, int R>
 MOE_DEV void dense_rows(const DenseEpi& e, int64_t m, int step, int n, float (&v)[R][8], float (&u)[R][8],
-                        const float (&b)[1][8], const u32x4* early = nullptr) {
+                        const float (&b)[1][8], float (&total)[8], const u32x4* early = nullptr) {
   float x[R][8];  // residual, upstream gradient or gate projection
   if (early != nullptr) {
 #pragma unroll
@@ -227,7 +229,10 @@ MOE_DEV void dense_rows(const DenseEpi& e, int64_t m, int step, int n, float (&v
     if (MODE == kEpiActBack) {
       act_slopes(e.act, v[k]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[k][i] *= x[k][i];
+      for (int i = 0; i < 8; ++i) {
+        v[k][i] *= x[k][i];
+        total[i] += v[k][i];
+      }
       store_planes(e, e.p0, o, v[k]);
     } else if (MODE == kEpiGated) {
       act_values(e.act, v[k]);
@@ -257,9 +262,9 @@ MOE_DEV void dense_rows(const DenseEpi& e, int64_t m, int step, int n, float (&v
 
 template <int MODE, bool INSIDE, int R>
 MOE_DEV void dense_epilogue(const DenseEpi& e, int64_t m, int step, int n, float (&v)[R][8], float (&u)[R][8],
-                            const float (&b)[1][8]) {
-  if (MODE == kEpiOut && e.residual) dense_rows<MODE, INSIDE, true, R>(e, m, step, n, v, u, b);
-  else dense_rows<MODE, INSIDE, false, R>(e, m, step, n, v, u, b);
+                            const float (&b)[1][8], float (&total)[8]) {
+  if (MODE == kEpiOut && e.residual) dense_rows<MODE, INSIDE, true, R>(e, m, step, n, v, u, b, total);
+  else dense_rows<MODE, INSIDE, false, R>(e, m, step, n, v, u, b, total);
 }
 
 // One element's planes
@@ -278,8 +283,9 @@ MOE_DEV float load1(const DenseEpi& e, const void* p, int64_t at) {
 }
 
 // The epilogue of one element, for a join whose lanes have one each.  Columns
-// from N to the next multiple of 8 are staged as zeros.
-template <int MODE> MOE_DEV void dense_epilogue1(const DenseEpi& e, int64_t m, int n, float v, float u) {
+// from N to the next multiple of 8 are staged as zeros.  kEpiActBack leaves its
+// unrounded result in v.
+template <int MODE> MOE_DEV void dense_epilogue1(const DenseEpi& e, int64_t m, int n, float& v, float u) {
   const bool in = n < e.N;
   if (MODE == kEpiOut) {
     if (!in) return;
@@ -299,8 +305,10 @@ template <int MODE> MOE_DEV void dense_epilogue1(const DenseEpi& e, int64_t m, i
     if (in) {
       if (e.bias) v += load1(e, e.bias, n);
       v = slope_one(e.act, v) * load1(e, e.dy, m * e.ld_dy + n);
+    } else {
+      v = 0.f;
     }
-    store_plane1(e, e.p0, o, in ? v : 0.f);
+    store_plane1(e, e.p0, o, v);
   } else {
     const float g = e.g[o], w = e.u[o], s = act_one(e.act, g);
     store_plane1(e, e.p0, o, in ? v * w * slope_one(e.act, g) : 0.f);
@@ -378,7 +386,8 @@ template <class S, class P> __global__ __launch_bounds__(kThreads, 1) void dense
 // eight (SHARES 8): lane k then adds up the parts k, k + 8, ... of all eight
 // columns, so that every part is in flight at once, the lanes' sums are added
 // in a fixed tree that leaves column k with lane k, and each lane finishes its
-// one element.
+// one element.  Where kEpiActBack's sums over the rows are wanted, its results
+// take the place of the first part's, which only these lanes have read.
 template <int MODE, int SHARES> __global__ __launch_bounds__(256) void dense_join_kernel(DenseGroup group) {
   constexpr bool DUAL = MODE == kEpiGated || MODE == kEpiKeep;
   const DenseArgs& g = group_args();
@@ -406,14 +415,16 @@ template <int MODE, int SHARES> __global__ __launch_bounds__(256) void dense_joi
     }
   }
   if (SHARES == 1) {
-    float b[1][8];
+    float b[1][8], total[8] = {};
     load_bias<MODE, false>(g.epi, n, b);
-    dense_epilogue<MODE, false, 1>(g.epi, m, 0, n, v, u, b);
+    dense_epilogue<MODE, false, 1>(g.epi, m, 0, n, v, u, b, total);
+    if (MODE == kEpiActBack && g.epi.sums) store_f32(g.part + m * g.ld_part + n, v[0]);
   } else {
     // halves are exchanged: lanes whose bit is set keep the upper columns
     scatter_sum(v[0], share);
     if (DUAL) scatter_sum(u[0], share);
     dense_epilogue1<MODE>(g.epi, m, n + share, v[0][0], u[0][0]);
+    if (MODE == kEpiActBack && g.epi.sums) g.part[m * g.ld_part + n + share] = v[0][0];
   }
 }
 
@@ -439,8 +450,8 @@ template <typename TE> __global__ __launch_bounds__(256) void dense_pack_kernel(
 // in 8 shares (share k: every eighth row from the k-th), joined in share order.
 constexpr int kSumRows = 64;  // rows of a workgroup
 template <typename TE>
-__global__ __launch_bounds__(256) void dense_colsum_kernel(const TE* src, int64_t ld, int n_planes, int64_t plane,
-                                                           int64_t rows, int cols, float* part) {
+__global__ __launch_bounds__(256) void dense_colsum_kernel(const TE* src, int64_t ld, int64_t rows, int cols,
+                                                           float* part) {
   __shared__ float acc[8][256];
   const int lane = threadIdx.x & 31, share = threadIdx.x >> 5;
   const int c = blockIdx.y * 256 + lane * 8;
@@ -450,13 +461,12 @@ __global__ __launch_bounds__(256) void dense_colsum_kernel(const TE* src, int64_
 #pragma unroll
   for (int i = 0; i < 8; ++i) s[i] = 0.f;
 #pragma unroll 8
-  for (int64_t r = r0 + share; r < r1; r += 8)
-    for (int p = 0; p < n_planes; ++p) {
-      float v[8];
-      load8<false>(src + p * plane + r * ld, c, cols, v);
+  for (int64_t r = r0 + share; r < r1; r += 8) {
+    float v[8];
+    load8<false>(src + r * ld, c, cols, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] += v[i];
-    }
+    for (int i = 0; i < 8; ++i) s[i] += v[i];
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[share][lane * 8 + i] = s[i];
   __syncthreads();
@@ -738,30 +748,55 @@ hipError_t launch_dense_pack(const PackJobs& jobs, int count, bool f32, hipStrea
   return hipGetLastError();
 }
 
-size_t dense_colsum_bytes(int64_t rows, int cols) {
-  return size_t((rows + kSumRows - 1) / kSumRows) * size_t(cols) * sizeof(float);
+// (a row of sums for each half of a tile's rows, or for each chunk of rows)
+size_t dense_sums_bytes(int64_t rows, int cols) {
+  return size_t((rows + kSumRows - 1) / kSumRows) * 2 * size_t(cols) * sizeof(float);
 }
 
-hipError_t launch_dense_colsum(const void* src, int64_t ld, int n_planes, int64_t plane, int64_t rows, int cols,
-                               void* out, bool f32, float* part, hipStream_t st) {
-  const int64_t chunks = (rows + kSumRows - 1) / kSumRows;
-  // chunks lie along x: there are up to 2^18 of them
-  const dim3 grid(unsigned(chunks), (cols + 255) / 256), join((cols + 31) / 32);
-  if (n_planes == 0)
-    hipLaunchKernelGGL((dense_colsum_kernel<float>), grid, dim3(256), 0, st, static_cast<const float*>(src), ld, 1,
-                       int64_t(0), rows, cols, part);
-  else
-    hipLaunchKernelGGL((dense_colsum_kernel<bf16_t>), grid, dim3(256), 0, st, static_cast<const bf16_t*>(src), ld,
-                       n_planes, plane, rows, cols, part);
-  const hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
+namespace {
+
+hipError_t join_sums(const float* sums, int64_t n, int cols, void* out, bool f32, hipStream_t st) {
+  const dim3 grid((cols + 31) / 32);
   if (f32)
-    hipLaunchKernelGGL((dense_colsum_join_kernel<float>), join, dim3(1024), 0, st, part, chunks, cols,
+    hipLaunchKernelGGL((dense_colsum_join_kernel<float>), grid, dim3(1024), 0, st, sums, n, cols,
                        static_cast<float*>(out));
   else
-    hipLaunchKernelGGL((dense_colsum_join_kernel<bf16_t>), join, dim3(1024), 0, st, part, chunks, cols,
+    hipLaunchKernelGGL((dense_colsum_join_kernel<bf16_t>), grid, dim3(1024), 0, st, sums, n, cols,
                        static_cast<bf16_t*>(out));
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_dense_colsum(const void* src, bool src_f32, int64_t ld, int64_t rows, int cols, void* out, bool f32,
+                               float* sums, hipStream_t st) {
+  const int64_t chunks = (rows + kSumRows - 1) / kSumRows;
+  // chunks lie along x: there are up to 2^18 of them
+  const dim3 grid(unsigned(chunks), (cols + 255) / 256);
+  if (src_f32)
+    hipLaunchKernelGGL((dense_colsum_kernel<float>), grid, dim3(256), 0, st, static_cast<const float*>(src), ld, rows,
+                       cols, sums);
+  else
+    hipLaunchKernelGGL((dense_colsum_kernel<bf16_t>), grid, dim3(256), 0, st, static_cast<const bf16_t*>(src), ld, rows,
+                       cols, sums);
+  const hipError_t err = hipGetLastError();
+  return err != hipSuccess ? err : join_sums(sums, chunks, cols, out, f32, st);
+}
+
+hipError_t launch_dense_act_back(const DenseArgs& args, void* dbias, float* sums, float* part, hipStream_t st) {
+  DenseGroup group{};
+  DenseArgs& g = group.g[0];
+  g = args;
+  if (dbias != nullptr) g.epi.sums = sums;
+  hipError_t err = launch_dense(group, 1, kNT, part, st);
+  if (err != hipSuccess || dbias == nullptr) return err;
+  const DensePlan p = dense_plan(g.M, g.N, g.K, g.segments, 0, 1, false);
+  if (p.split > 1) {
+    set_plan(g, p, part);
+    return launch_dense_colsum(part, true, g.ld_part, g.M, g.N, dbias, g.epi.f32, sums, st);
+  }
+  const int64_t rows = std::max(p.tile, 64);
+  return join_sums(sums, (g.M + rows - 1) / rows * 2, g.N, dbias, g.epi.f32, st);
 }
 
 }  // namespace moe
