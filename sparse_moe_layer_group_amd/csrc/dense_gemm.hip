@@ -434,16 +434,17 @@ template <int MODE, int SHARES> __global__ __launch_bounds__(256) void dense_joi
 template <typename TE> __global__ __launch_bounds__(256) void dense_pack_kernel(PackJobs jobs) {
   typedef const __attribute__((address_space(4))) PackJobs* Args;
   const PackJob& j = ((const PackJobs*)(Args)__builtin_amdgcn_kernarg_segment_ptr())->j[blockIdx.y];
-  const int64_t per = j.ld_dst / 8, id = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t r = id / per;
-  if (r >= j.rows) return;
-  const int c = int(id - r * per) * 8;
-  float v[8];
-  load8<false>(static_cast<const TE*>(j.src) + r * j.ld_src, c, j.cols, v);
-  DenseEpi e{};
-  e.f32 = sizeof(TE) == 4;
-  e.plane = j.rows * j.ld_dst;
-  store_planes(e, j.dst, r * j.ld_dst + c, v);
+  const int64_t per = j.ld_dst / 8, all = j.rows * per;
+  for (int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x; id < all; id += int64_t(gridDim.x) * 256) {
+    const int64_t r = id / per;
+    const int c = int(id - r * per) * 8;
+    float v[8];
+    load8<false>(static_cast<const TE*>(j.src) + r * j.ld_src, c, j.cols, v);
+    DenseEpi e{};
+    e.f32 = sizeof(TE) == 4;
+    e.plane = j.rows * j.ld_dst;
+    store_planes(e, j.dst, r * j.ld_dst + c, v);
+  }
 }
 
 // Column sums.  A workgroup takes 256 columns, 8 a thread, and a range of rows
@@ -568,7 +569,7 @@ template <class S> int64_t tiles_of(const DenseArgs& g) {
 
 hipError_t launch_kernel(void (*kernel)(DenseGroup), int lds, int64_t tiles, const DenseGroup& group, int count,
                          hipStream_t st) {
-  if (tiles >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+  if (tiles * kThreads >= (int64_t(1) << 32)) return hipErrorInvalidValue;  // of a grid dimension
   const hipError_t err =
       hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (err != hipSuccess) return err;
@@ -739,8 +740,9 @@ hipError_t launch_dense_pack(const PackJobs& jobs, int count, bool f32, hipStrea
   if (count < 0 || count > kMaxPacks) return hipErrorInvalidValue;
   int64_t blocks = 0;
   for (int i = 0; i < count; ++i) blocks = std::max(blocks, (jobs.j[i].rows * (jobs.j[i].ld_dst / 8) + 255) / 256);
-  if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
   if (blocks == 0) return hipSuccess;
+  // (a grid dimension has less than 2^32 threads; past these the blocks go on)
+  blocks = std::min(blocks, int64_t(1) << 22);
   if (f32)
     hipLaunchKernelGGL((dense_pack_kernel<float>), dim3(unsigned(blocks), unsigned(count)), dim3(256), 0, st, jobs);
   else
