@@ -285,9 +285,9 @@ int moe_quantize_1x128(const void* x, int64_t rows, int32_t cols, uint8_t* q, fl
  *    MOE_ERR_DTYPE): activations, parameters and their gradients.  Everything
  *    between is float32 or, for the operands of a later product, rounded once
  *    to bfloat16 (F32: not rounded; products of float32 operands keep float32's
- *    precision).  Parameter gradients have their parameter's type: those of
- *    products are made of bfloat16 operands, whose rounding a wider store
- *    would only preserve.
+ *    precision).  Parameter gradients have their parameter's type and are
+ *    rounded to it once, from float32 sums: a caller who adds up bfloat16 ones
+ *    over several batches rounds each (moe_backward's are float32).
  *  - Activations are rows of contiguous elements, `ld_*` elements apart: any
  *    ld >= the row's length and < 2^22 (else MOE_ERR_SHAPE), so columns of a
  *    wider tensor can be passed; pointers are aligned to their element.
@@ -466,7 +466,9 @@ const char* moe_profile_kernel_name(int slot);
 /* Static description of a status code. */
 const char* moe_status_string(int status);
 
-/* ABI version (major * 100 + minor). */
+/* ABI version (major * 100 + minor) of the entry points' arguments and structs.
+ * An entry point that was added changes neither: its symbol says whether it is
+ * there. */
 int moe_abi_version(void);
 
 #ifdef __cplusplus

@@ -221,10 +221,12 @@ hipError_t launch(const moe::DenseArgs& g, int layout, float* part, hipStream_t 
 }
 
 // Whether a forward product goes to the weight-streaming kernel.  bfloat16: up
-// to 16 tokens, one MFMA's (a block of hidden 7168 and inter 2048 from memory:
-// one token 24.9 us, 8 26.4, 16 28.7, by tiles 29.1 for 17; 32 tokens 42 us
-// against 28.8 by tiles).  float32: to 64, as the tiles need the weights laid
-// out as three planes first (130 against 182 us).
+// to 16 tokens, one MFMA's (a block of hidden 7168 and inter 2048, weights from
+// memory: one token 24.9 us against 26.7 by tiles, 8 26.5 against 26.8, 16 28.6
+// against 27.0, 17 31.1 against 27.9, 32 39 against 29; weights of odd rows or
+// unaligned ones it takes as they are, where the tiles need a copy).  float32:
+// to 64, as the tiles need the weights laid out as three planes first (one token
+// 46 us against 157, 64 tokens 129 against 178).
 bool streams(int64_t T, bool f32) { return T <= (f32 ? moe::kStreamTokens : 16); }
 
 // ---------------------------------------------------------------- linear

@@ -27,14 +27,15 @@
 // of row r at c ^ (r & 7)), a k-slow one as k-rows of TM or TN columns, read
 // with the transposing ds_read_b64_tr_b16; neither has bank conflicts.
 //
-// Measured, bfloat16, M x N x K (the library's product, which has no epilogue,
-// in brackets): 8192 x 4096 x 7168 312 us = 1.54 PFLOP/s (302), 4096 x 7168 x
-// 7168 293 us (280), 8192 x 7168 x 2048 197 us (179), 4096 x 2048 x 7168 99 us
-// (97).  Counters for the first: MFMAs busy 76% of the cycles at 1.80 GHz; 82%
-// without copies and reads.  What is left is 4 us before a tile's first MFMA and
-// 8 us for its epilogue, with nothing to overlap them: a workgroup that went on
-// to its next tile instead was slower (its loop had waits that depend on the
-// tile), so was an epilogue without LDS (rows of 64 bytes a store: 197 -> 205 us).
+// Measured, bfloat16, M x N x K, operands changing from call to call (the
+// library's product, which has no epilogue, in brackets): 8192 x 4096 x 7168 318
+// us = 1.51 PFLOP/s (306), 4096 x 7168 x 7168 296 us (288), 8192 x 7168 x 2048
+// 191 us (170 to 176), 4096 x 2048 x 7168 113 us (102).  Counters for the first:
+// MFMAs busy 76% of the cycles at 1.80 GHz; 82% without copies and reads.  What
+// is left is 4 us before a tile's first MFMA and 8 us for its epilogue, with
+// nothing to overlap them: a workgroup that went on to its next tile instead was
+// slower (its loop had waits that depend on the tile), so was an epilogue without
+// LDS (rows of 64 bytes a store: 8192 x 7168 x 2048 198 -> 205 us).
 //
 // Bounds.  An operand's buffer resource starts at the step's own first element
 // and ends with the matrix, so rows past the end read as zero without a
@@ -57,7 +58,6 @@ typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef short v8i16 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
-typedef __attribute__((address_space(3))) float lds_f32;
 typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 
 // s_waitcnt immediates: vmcnt(0) and lgkmcnt(0); vmcnt(n)
@@ -517,7 +517,9 @@ int64_t tiles_of(int64_t M, int64_t N, int dual, int tile) {
 // with two on the CU.  Measured on A B^T products of 16 to 8192 rows, 200 to
 // 7168 columns and contractions of 512 to 16384, every tile and split of each:
 // the sum below is within 10% of most of them and the choice it makes within
-// 10% of the best.
+// 10% of the best.  A B, A^T B and the epilogues that read and write more take
+// the same figures, which are too low for some (the gated backward of 4096 x 2048
+// x 7168 by 128 x 128: 110 us here, 134 measured).
 struct TileCost {
   int tile, per_cu;
   double step[2], once;
@@ -532,7 +534,7 @@ constexpr double kJoinOnce = 5.5, kJoinBytesPerUs = 4.5e6;  // of a split contra
 // few tiles, and every split is paid for with its sums' way through memory.
 // narrow: the 64 x 32 tile is there, for forward products of few tokens, whose
 // weights should pass through as many CUs as there are (50 tokens by 7168 rows
-// of 2048: 11.3 us against 13.5 by 64 x 64 and as much by a split).
+// of 2048: 10.8 us against 13.1 by what the other tiles and splits give).
 // M counts in whole 64 rows, so that one plan holds for each 64 (dense_part_most).
 constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
 constexpr int kSplitGroups = 1024;  // a split leaves at most so many workgroups
@@ -700,9 +702,11 @@ hipError_t launch_dense(const DenseGroup& args, int count, int layout, float* pa
 
 // A layer's gradients of its input (A B) and of its weights (A^T B).  Where both
 // take the small tile and fit the chip together they go in one launch: 300 x
-// 1024 x 256 in float32 24.4 -> 15.4 us, 512 x 1024 x 1024 in bfloat16 12.8 ->
-// 8.3.  (With more workgroups than fit, the one launch is slower: a feed-forward
-// block of 512 x 1024 x 1024 39.0 us against 37.2.)
+// 1024 x 256 in float32 25.1 -> 15.5 us, 512 x 1024 x 1024 in bfloat16 13.0 ->
+// 8.2, a feed-forward block of 300 x 1024 x 256 28.6 -> 23.4.  With more
+// workgroups than fit it is slower for some (300 x 1024 x 2048 in float32 44.9 ->
+// 46.5) and faster for others (512 x 1536 x 1024 in bfloat16 14.7 -> 10.9); those
+// are not told apart here and stay in two.
 hipError_t launch_dense_gradients(const DenseArgs& data, const DenseGroup& weights, int count, float* part,
                                   hipStream_t st) {
   if (count < 1 || count >= kMaxGroup) return hipErrorInvalidValue;

@@ -14,10 +14,12 @@
 // of them against 16 tokens.  float32 operands are split in registers into
 // three bfloat16 parts (exactly) and multiplied as six MFMAs.
 //
-// Measured, one token, bfloat16: 2 x 2048 rows of 7168 in 13 us = 4.5 TB/s,
-// 7168 rows of 2048 in 8.6 us = 3.4 TB/s; a launch that reads nothing takes 3.5.
+// Measured, one token, bfloat16: 2 x 2048 rows of 7168 in 13.5 us = 4.4 TB/s,
+// 7168 rows of 2048 in 8.8 us = 3.3 TB/s; a launch that reads nothing takes 3.5.
 // From 17 tokens on the loads of the tokens themselves, which every workgroup
-// repeats, are what bounds it (32 tokens through both: 42 us, by tiles 32).
+// repeats, are what bounds it (32 tokens through both: 39 us, by tiles 29), in
+// float32 with splitting them again in every workgroup (one token 46 us, 16 56,
+// 32 79, 64 129).
 #include "block.h"
 
 namespace moe {

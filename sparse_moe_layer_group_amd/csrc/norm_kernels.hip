@@ -30,14 +30,22 @@
 // the backward's registers are short (layer norm, float32, ragged and wide
 // rows), the weights are read again for every row, from the caches, and past
 // 8192 the next row is not fetched ahead: 4096 rows of 7168 with a layer norm
-// 340 -> 130 us, 2048 of 16384 with an RMS norm 722 -> 170 us.
+// 340 -> 127 us, 2048 of 16384 with an RMS norm 722 -> 174 us.  That is not
+// enough everywhere: of float32 past 1024 the backward's layer norm and ragged
+// RMS norm put 5 to 61 registers out to memory, every backward past 8192 63 to
+// 248, and there the forward of float32 36 (ragged) to 174 (layer norm).
 //
 // Measured: forward, 8192 rows of 7168 in bfloat16, 96 us = 4.9 TB/s, what a
-// large copy reaches on this card (5.0); one row 4 us, a launch's latency.
+// large copy reaches on this card (5.0), as a layer norm 99, float32 191 either
+// way, without gate and first norm 95; one row 4 us, a launch's latency.
 // Backward, 4096 rows of 7168 in bfloat16, RMS: 80 us = 4.4 TB/s and 6 us for
-// the join; as a layer norm 130 us, float32 165 us.  777 rows of 1001 in
-// float32, layer norm: 10 + 5 us.  Of the backward's 80 us the sums' barriers
-// and the column gradients' arithmetic are what is above the copy's 70.
+// the join; as a layer norm 127 us (six rounds of sums a row and the parameters
+// again, several times a row), float32 174 and 235.  2048 rows of 16384: forward
+// 57, float32 layer norm 189; backward 174, as a layer norm 460, float32 476, all
+// by the registers put out.  777 rows of 1001 in float32, layer norm: 11 + 4.5
+// us, the time that one wave takes for its row or two.  Of the backward's 80 us
+// the sums' barriers and the column gradients' arithmetic are what is above the
+// copy's 70.
 #include "block.h"
 
 namespace moe {
@@ -237,7 +245,7 @@ template <typename TE_, int NV_, bool ONE_WAVE_, bool LAYER_, bool WHOLE_> struc
   static constexpr int NV = NV_;
   static constexpr bool ONE_WAVE = ONE_WAVE_, LAYER = LAYER_, WHOLE = WHOLE_;
   // backward: the parameters are read again for every row (from the caches)
-  // where keeping them would put other registers out to memory
+  // where keeping them would put (more) other registers out to memory
   static constexpr bool REREAD = !ONE_WAVE && (LAYER || !WHOLE || NV > 2 || sizeof(TE) == 4);
   // ... and the next row is not kept in flight
   static constexpr bool FETCH_AHEAD = NV <= 2;
