@@ -270,9 +270,9 @@ struct DenseArgs {
 // launch (the gate, up and down matrices' gradients).
 constexpr int kMaxGroup = 4;  // these and a data gradient
 struct DenseGroup { DenseArgs g[kMaxGroup]; };
-// Room for the sums of a split contraction: of this product; and enough for it
-// with any smaller M, or with any smaller K (A^T B)
-size_t dense_part_bytes(int64_t M, int N, int64_t K, int segments, int dual, int count);
+// Room for the sums of a split contraction: of this product (thin: it may take the
+// 64 x 32 tile); and enough for it with any smaller M, or any smaller K (A^T B)
+size_t dense_part_bytes(int64_t M, int N, int64_t K, int segments, int dual, int count, bool thin);
 size_t dense_part_most(int64_t M, int N, int64_t K, int segments, int dual, int count);
 size_t dense_part_most_deep(int64_t M, int N, int64_t K, int segments, int count);
 hipError_t launch_dense(const DenseGroup& group, int count, int layout, float* part, hipStream_t st);

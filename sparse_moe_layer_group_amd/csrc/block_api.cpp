@@ -206,12 +206,12 @@ enum Batches { kThis, kUpTo };
 // room for split sums of a product with T rows, and of one that contracts over T
 size_t rows_part(Batches b, int64_t T, int N, int64_t K, bool f32, int pairs = 1, int dual = 0) {
   const int segments = pairs * (f32 ? kPairs : 1);
-  return b == kThis ? moe::dense_part_bytes(T, N, K, segments, dual, 1)
+  return b == kThis ? moe::dense_part_bytes(T, N, K, segments, dual, 1, true)
                     : moe::dense_part_most(T, N, K, segments, dual, 1);
 }
 size_t deep_part(Batches b, int64_t M, int N, int64_t T, bool f32, int count = 1) {
   const int segments = f32 ? kPairs : 1;
-  return b == kThis ? moe::dense_part_bytes(M, N, T, segments, 0, count)
+  return b == kThis ? moe::dense_part_bytes(M, N, T, segments, 0, count, false)
                     : moe::dense_part_most_deep(M, N, T, segments, count);
 }
 hipError_t launch(const moe::DenseArgs& g, int layout, float* part, hipStream_t st) {

@@ -621,14 +621,14 @@ int64_t part_floats(const DensePlan& p, int64_t M, int N, int dual) {
 
 }  // namespace
 
-size_t dense_part_bytes(int64_t M, int N, int64_t K, int segments, int dual, int count) {
-  int64_t floats = 0;
-  for (bool thin : {false, true})
-    floats = std::max(floats, part_floats(dense_plan(M, N, K, segments, dual, count, thin && !dual), M, N, dual));
+size_t dense_part_bytes(int64_t M, int N, int64_t K, int segments, int dual, int count, bool thin) {
+  int64_t floats = part_floats(dense_plan(M, N, K, segments, dual, count, false), M, N, dual);
+  if (thin && !dual)
+    floats = std::max(floats, part_floats(dense_plan(M, N, K, segments, dual, count, true), M, N, dual));
   return size_t(count) * size_t(floats) * sizeof(float);
 }
 
-// The most that dense_part_bytes gives for any M from 1 to this one: the plan
+// The most that dense_part_bytes (thin) gives for any M from 1 to this one: the plan
 // is the same for 64 rows at a time, and the last of them take the most.
 size_t dense_part_most(int64_t M, int N, int64_t K, int segments, int dual, int count) {
   size_t most = 0;
@@ -636,12 +636,12 @@ size_t dense_part_most(int64_t M, int N, int64_t K, int segments, int dual, int 
   for (int64_t m = 64;; m += 64) {
     const int64_t at = std::min(m, M);
     if (tiles_of(at, N, dual, kTileCosts[0].tile) * count * kSplits[1] > kSplitGroups) return most;  // nor further on
-    most = std::max(most, dense_part_bytes(at, N, K, segments, dual, count));
+    most = std::max(most, dense_part_bytes(at, N, K, segments, dual, count, true));
     if (at == M) return most;
   }
 }
 
-// At least what dense_part_bytes gives for any K up to this one.  A split into u
+// At least what dense_part_bytes (not thin) gives for any K up to this one.  A split into u
 // parts takes per >= steps / u steps a part, so where the turns of the chip that
 // its groups take cost no less, divided by u, than the whole product's, the
 // whole product (no join) always costs less.
@@ -650,7 +650,7 @@ size_t dense_part_most_deep(int64_t M, int N, int64_t K, int segments, int count
   int most = 1;
   for (const TileCost& c : kTileCosts) {
     const int64_t tiles = tiles_of(M, N, 0, c.tile) * count, slots = int64_t(256) * c.per_cu;
-    if (c.tile == 32) break;  // forward products only
+    if (c.tile == 32) break;
     auto turns = [&](int u) {  // microseconds that a step of every group takes
       const int64_t rest = tiles * u % slots;
       return double(tiles * u / slots) * c.step[c.per_cu - 1] + (rest == 0 ? 0.0 : c.step[rest > 256 ? 1 : 0]);
