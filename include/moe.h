@@ -448,6 +448,110 @@ int moe_ffn_backward(const moe_ffn_cfg* cfg, int64_t T, const void* x, int64_t l
                      void* dw_down, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Microscaled operands: quantisation, the norm that leaves its output in this
+ * form, and projections and the gated feed-forward block with 4-bit weights
+ * that read it.  The conventions of the operators around the expert layer hold;
+ * dtype is the type of every tensor of a call that is not microscaled.
+ *
+ * Blocks of 32 consecutive elements of a row share a power of two (the format
+ * of the OCP Microscaling specification, version 1.0):
+ *   value = element * 2^e, e = max(floor(log2(largest |v| of the block)) - emax, -127)
+ *   element = v 2^-e rounded to nearest, ties to even, saturated
+ * A block of zeros has e = -127, one with a NaN or an infinity is NaN throughout.
+ * Layout of [rows][cols]: rows are padded to S = ceil(cols / 128) steps of 128
+ * elements, packed;
+ *   codes  [rows][S * 128] bytes (E4M3) or [rows][S * 64] (E2M1: the even
+ *          element in the low four bits), aligned to 16 bytes
+ *   scales [rows][S * 4] bytes, aligned to 4 (else MOE_ERR_SHAPE): e + 127 of
+ *          each block, 255 for NaN
+ * Codes of padding are 0 and its scales not 255: the writers here leave them so,
+ * products read them.  Wholly padded blocks are written as blocks of zeros.
+ * rows <= 2^24, cols 1 .. 131072, else MOE_ERR_SHAPE; another format: MOE_ERR_DTYPE.
+ */
+enum moe_mx_format {
+  MOE_MX_E4M3 = 0, /* 8 bits: OCP E4M3FN, emax 8, largest 448 */
+  MOE_MX_E2M1 = 1  /* 4 bits: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign, emax 2 */
+};
+
+/* Bytes of codes and of scales (0 for what is invalid). */
+size_t moe_mx_code_bytes(int32_t format, int64_t rows, int32_t cols);
+size_t moe_mx_scale_bytes(int64_t rows, int32_t cols);
+
+/* x: device [rows][cols] of dtype (F32 or BF16), rows ld_x apart, to codes and scales. */
+int moe_mx_quantize(int32_t format, int32_t dtype, int64_t rows, int32_t cols, const void* x,
+                    int64_t ld_x, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* The values, rounded once to dtype (which holds them exactly but for the
+ * smallest and largest scales), to y: device [rows][cols]. */
+int moe_mx_dequantize(int32_t format, int32_t dtype, int64_t rows, int32_t cols,
+                      const uint8_t* codes, const uint8_t* scales, void* y, int64_t ld_y,
+                      void* stream);
+
+/*
+ * moe_norm_forward with h in microscaled form.
+ *   codes, scales  out, [T][hidden], formed from the unrounded h; required
+ *   u, h           out, [T][hidden] of cfg's dtype, or NULL each
+ * u and h may be residual or branch as in moe_norm_forward.
+ */
+int moe_norm_mx_forward(const moe_norm_cfg* cfg, int32_t format, int64_t T, const void* residual,
+                        int64_t ld_residual, const void* branch, int64_t ld_branch,
+                        const moe_norm_params* params, void* u, int64_t ld_u, void* h, int64_t ld_h,
+                        uint8_t* codes, uint8_t* scales, void* stream);
+
+/* A microscaled operand (device pointers; the struct is host memory). */
+typedef struct moe_mx {
+  const uint8_t* codes;
+  const uint8_t* scales;
+} moe_mx;
+
+/* A projection: in_dim -> out_dim (1 .. 131072 each, else MOE_ERR_SHAPE), any moe_act. */
+typedef struct moe_mx_linear_cfg {
+  int32_t in_dim;
+  int32_t out_dim;
+  int32_t act;     /* moe_act, else MOE_ERR_SHAPE */
+  int32_t dtype;   /* moe_dtype of bias, residual and y: F32 or BF16 */
+  int32_t format;  /* moe_mx_format of x; the weights are E2M1 */
+} moe_mx_linear_cfg;
+
+/*
+ * y = residual + act(x W^T + bias), sums in float32.  What the matrix cores make
+ * of E4M3 operands loses 1e-5 to 2e-5 of a sum, which bfloat16 outputs do not
+ * show; with float32 ones (dtype F32) they are multiplied in three exact parts,
+ * at a third of the rate.  Products below 2^-149 count as 0.
+ *   x         [T][in_dim] in cfg's format;  w: [out_dim][in_dim] in E2M1
+ *   bias      [out_dim] or NULL;   residual: [T][out_dim] or NULL
+ *   y         out [T][out_dim]; may be residual itself (same ld)
+ */
+size_t moe_mx_linear_workspace_bytes(const moe_mx_linear_cfg* cfg, int64_t T);
+int moe_mx_linear_forward(const moe_mx_linear_cfg* cfg, int64_t T, const moe_mx* x, const moe_mx* w,
+                          const void* bias, const void* residual, int64_t ld_residual, void* y,
+                          int64_t ld_y, void* ws, size_t ws_bytes, void* stream);
+
+/* A dense gated feed-forward block hidden -> inter -> hidden (1 .. 131072
+ * each); act: RELU, SILU or GELU, else MOE_ERR_SHAPE. */
+typedef struct moe_mx_ffn_cfg {
+  int32_t hidden;
+  int32_t inter;
+  int32_t act;     /* moe_act */
+  int32_t dtype;   /* moe_dtype of residual and y: F32 or BF16 */
+  int32_t format;  /* moe_mx_format of x and of the block's middle; the weights are E2M1 */
+} moe_mx_ffn_cfg;
+
+/*
+ * y = residual + m Wd^T, m = act(x Wg^T) * (x Wu^T) in cfg's format, formed from
+ * the unrounded product.
+ *   x            [T][hidden] in cfg's format
+ *   w_gate, w_up [inter][hidden], w_down [hidden][inter] in E2M1
+ *   residual     [T][hidden] or NULL;  y: out, may be residual itself (same ld)
+ */
+size_t moe_mx_ffn_workspace_bytes(const moe_mx_ffn_cfg* cfg, int64_t T);
+int moe_mx_ffn_forward(const moe_mx_ffn_cfg* cfg, int64_t T, const moe_mx* x, const moe_mx* w_gate,
+                       const moe_mx* w_up, const moe_mx* w_down, const void* residual,
+                       int64_t ld_residual, void* y, int64_t ld_y, void* ws, size_t ws_bytes,
+                       void* stream);
+
+/*
  * Kernel timing instrumentation (off by default).  The state is per host
  * thread: moe_profile_enable switches it for the calling thread, whose
  * compute calls then record, and moe_profile_read reads that thread's record.

@@ -8,13 +8,15 @@ raise.
 Entry points mirror the C ABI in ``include/moe.h``: :func:`workspace_bytes`,
 :func:`route`, :func:`forward`, :func:`bias_update`; and, around the expert
 layer, :func:`norm_forward` / :func:`norm_backward`, :func:`linear_forward` /
-:func:`linear_backward` and :func:`ffn_forward` / :func:`ffn_backward`.
+:func:`linear_backward` and :func:`ffn_forward` / :func:`ffn_backward`; with microscaled operands
+(:class:`MxMatrix`) :func:`mx_quantize` / :func:`mx_dequantize`, :func:`norm_mx_forward`,
+:func:`mx_linear_forward` and :func:`mx_ffn_forward`.
 """
 from __future__ import annotations
 
 import ctypes
 import os
-from typing import Dict, Optional
+from typing import Dict, NamedTuple, Optional
 
 import torch
 
@@ -30,7 +32,11 @@ __all__ = ["F32", "BF16", "E4M3", "MoeError", "lib", "lib_path", "make_cfg", "cf
            "linear_backward_workspace_bytes", "alloc_linear_workspace",
            "alloc_linear_backward_workspace",
            "make_ffn_cfg", "ffn_forward", "ffn_backward", "ffn_workspace_bytes",
-           "ffn_backward_workspace_bytes", "alloc_ffn_workspace", "alloc_ffn_backward_workspace"]
+           "ffn_backward_workspace_bytes", "alloc_ffn_workspace", "alloc_ffn_backward_workspace",
+           "MxMatrix", "alloc_mx", "mx_quantize", "mx_dequantize", "norm_mx_forward",
+           "make_mx_linear_cfg", "mx_linear_forward", "mx_linear_workspace_bytes",
+           "alloc_mx_linear_workspace", "make_mx_ffn_cfg", "mx_ffn_forward",
+           "mx_ffn_workspace_bytes", "alloc_mx_ffn_workspace"]
 
 F32, BF16, E4M3 = 0, 1, 2
 _DT_NAME = {"f32": F32, "bf16": BF16, "e4m3": E4M3}
@@ -44,7 +50,11 @@ EXPORTED_SYMBOLS = ("moe_workspace_bytes", "moe_route", "moe_forward", "moe_bias
                     "moe_norm_forward", "moe_norm_backward", "moe_norm_backward_workspace_bytes",
                     "moe_linear_forward", "moe_linear_backward", "moe_linear_workspace_bytes",
                     "moe_linear_backward_workspace_bytes", "moe_ffn_forward", "moe_ffn_backward",
-                    "moe_ffn_workspace_bytes", "moe_ffn_backward_workspace_bytes")
+                    "moe_ffn_workspace_bytes", "moe_ffn_backward_workspace_bytes",
+                    "moe_mx_code_bytes", "moe_mx_scale_bytes", "moe_mx_quantize",
+                    "moe_mx_dequantize", "moe_norm_mx_forward", "moe_mx_linear_forward",
+                    "moe_mx_linear_workspace_bytes", "moe_mx_ffn_forward",
+                    "moe_mx_ffn_workspace_bytes")
 NOALLOC_SCRATCH_BYTES = 64 << 20    # MOE_NOALLOC_SCRATCH_BYTES of include/moe.h
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -104,6 +114,22 @@ class _FfnCfg(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("hidden", "inter", "act", "dtype")]
 
 
+_MX_FORM = {"e4m3": 0, "e2m1": 1}                          # enum moe_mx_format
+_MX_STEP = (128, 64)                                       # bytes of 128 codes, by format
+
+
+class _Mx(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class _MxLinearCfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("in_dim", "out_dim", "act", "dtype", "format")]
+
+
+class _MxFfnCfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("hidden", "inter", "act", "dtype", "format")]
+
+
 _LIB: Optional[ctypes.CDLL] = None
 
 
@@ -159,14 +185,24 @@ def lib() -> ctypes.CDLL:
                 ("linear_forward", [C(_LinearCfg), I64, P, V, P, P, P, V, P, V, P, SZ, P]),
                 ("linear_backward", [C(_LinearCfg), I64, P, V, P, P, P, V, P, V, P, P, P, SZ, P]),
                 ("ffn_forward", [C(_FfnCfg), I64, P, V, P, P, P, P, V, P, V, P, SZ, P]),
-                ("ffn_backward", [C(_FfnCfg), I64, P, V, P, P, P, P, V, P, V, P, P, P, P, SZ, P])):
+                ("ffn_backward", [C(_FfnCfg), I64, P, V, P, P, P, P, V, P, V, P, P, P, P, SZ, P]),
+                ("mx_quantize", [I32, I32, I64, I32, P, V, P, P, P]),
+                ("mx_dequantize", [I32, I32, I64, I32, P, P, P, V, P]),
+                ("norm_mx_forward", [C(_NormCfg), I32, I64, P, V, P, V, C(_NormParams), P, V, P, V,
+                                     P, P, P]),
+                ("mx_linear_forward", [C(_MxLinearCfg), I64, C(_Mx), C(_Mx), P, P, V, P, V, P, SZ, P]),
+                ("mx_ffn_forward", [C(_MxFfnCfg), I64, C(_Mx), C(_Mx), C(_Mx), C(_Mx), P, V, P, V, P,
+                                    SZ, P])):
             fn = getattr(L, "moe_" + name)
             fn.argtypes, fn.restype = args, I32
         for name, cfg in (("norm_backward", _NormCfg), ("linear", _LinearCfg),
                           ("linear_backward", _LinearCfg), ("ffn", _FfnCfg),
-                          ("ffn_backward", _FfnCfg)):
+                          ("ffn_backward", _FfnCfg), ("mx_linear", _MxLinearCfg),
+                          ("mx_ffn", _MxFfnCfg)):
             fn = getattr(L, f"moe_{name}_workspace_bytes")
             fn.argtypes, fn.restype = [C(cfg), I64], SZ
+        L.moe_mx_code_bytes.argtypes, L.moe_mx_code_bytes.restype = [I32, I64, I32], SZ
+        L.moe_mx_scale_bytes.argtypes, L.moe_mx_scale_bytes.restype = [I64, I32], SZ
         _LIB = L
     return _LIB
 
@@ -648,3 +684,132 @@ def ffn_backward(cfg: _FfnCfg, x: torch.Tensor, weights: Dict[str, torch.Tensor]
           _packed(_need(dw_gate, "dw_gate"), "dw_gate", dt, I, H),
           _packed(_need(dw_up, "dw_up"), "dw_up", dt, I, H),
           _packed(_need(dw_down, "dw_down"), "dw_down", dt, H, I), *_ws(ws), _queue(stream))
+
+
+# ---------------------------------------------------------------- microscaled operands
+
+
+class MxMatrix(NamedTuple):
+    """A [rows][cols] matrix in microscaled form: uint8 tensors of codes ([rows][S * 128] for "e4m3",
+    [rows][S * 64] for "e2m1", S = ceil(cols / 128)) and of scales ([rows][S * 4])."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    form: str
+    cols: int
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+
+def alloc_mx(rows: int, cols: int, form: str = "e4m3", device="cuda") -> MxMatrix:
+    """Room for a matrix in microscaled form."""
+    steps = -(-cols // 128)
+    return MxMatrix(torch.empty((rows, steps * _MX_STEP[_MX_FORM[form]]), dtype=torch.uint8, device=device),
+                    torch.empty((rows, steps * 4), dtype=torch.uint8, device=device), form, cols)
+
+
+def _mx(m: Optional[MxMatrix], name: str, rows: int, cols: int, form: int):
+    """(codes, scales) pointers of a matrix of this size and form."""
+    if m is None:
+        raise ValueError(f"{name} is required")
+    if m.cols != cols or _MX_FORM.get(m.form) != form:
+        raise ValueError(f"{name}: {m.cols} columns of {m.form}, expected {cols} of "
+                         f"{'e4m3' if form == 0 else 'e2m1'}")
+    steps = -(-cols // 128)
+    return (_packed(m.codes, f"{name}.codes", torch.uint8, rows, steps * _MX_STEP[form]),
+            _packed(m.scales, f"{name}.scales", torch.uint8, rows, steps * 4))
+
+
+def _mx_tensor(t: torch.Tensor, name: str) -> int:
+    if t is None or t.dim() != 2:
+        raise ValueError(f"{name}: a matrix is required")
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.float32 or torch.bfloat16")
+    return F32 if t.dtype == torch.float32 else BF16
+
+
+def _form(m: MxMatrix) -> int:
+    if m is None or m.form not in _MX_FORM:
+        raise ValueError("a microscaled matrix of form 'e4m3' or 'e2m1' is required")
+    return _MX_FORM[m.form]
+
+
+def mx_quantize(x: torch.Tensor, out: MxMatrix, stream=None) -> None:
+    """moe_mx_quantize: the codes and scales of x ([rows][cols], float32 or bfloat16) into ``out``."""
+    dt, form = _mx_tensor(x, "x"), _form(out)
+    rows, cols = x.shape
+    _call("moe_mx_quantize", form, dt, rows, cols, *_rows(x, "x", x.dtype, rows, cols),
+          *_mx(out, "out", rows, cols, form), _queue(stream))
+
+
+def mx_dequantize(m: MxMatrix, y: torch.Tensor, stream=None) -> None:
+    """moe_mx_dequantize: the values of ``m`` into y ([rows][cols], float32 or bfloat16)."""
+    dt, form = _mx_tensor(y, "y"), _form(m)
+    rows, cols = y.shape
+    _call("moe_mx_dequantize", form, dt, rows, cols, *_mx(m, "m", rows, cols, form),
+          *_rows(y, "y", y.dtype, rows, cols), _queue(stream))
+
+
+def norm_mx_forward(cfg: _NormCfg, residual: torch.Tensor, branch: Optional[torch.Tensor],
+                    params: Dict[str, Optional[torch.Tensor]], u: Optional[torch.Tensor],
+                    out: MxMatrix, h: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_norm_mx_forward: :func:`norm_forward` with h in microscaled form into ``out`` (and, where
+    given, as it is into ``h``)."""
+    T, H, dt = _need(residual, "residual").shape[0], cfg.hidden, _TORCH_DT[cfg.dtype]
+    form = _form(out)
+    p = _norm_params(cfg, T, dt, params)
+    _call("moe_norm_mx_forward", cfg, form, T, *_rows(residual, "residual", dt, T, H),
+          *_rows(branch, "branch", dt, T, H), p, *_rows(u, "u", dt, T, H), *_rows(h, "h", dt, T, H),
+          *_mx(out, "out", T, H, form), _queue(stream))
+
+
+def make_mx_linear_cfg(in_dim: int, out_dim: int, act: str = "none", dtype=BF16,
+                       form: str = "e4m3") -> _MxLinearCfg:
+    """moe_mx_linear_cfg; dtype of bias, residual and y, form of x (the weights are "e2m1")."""
+    return _MxLinearCfg(in_dim, out_dim, _ACT.get(act, act), _DT_NAME.get(dtype, dtype),
+                        _MX_FORM.get(form, form))
+
+
+def mx_linear_workspace_bytes(cfg: _MxLinearCfg, T: int) -> int:
+    return int(lib().moe_mx_linear_workspace_bytes(ctypes.byref(cfg), int(T)))
+
+
+def alloc_mx_linear_workspace(cfg: _MxLinearCfg, T: int, device="cuda") -> torch.Tensor:
+    return _alloc("mx_linear", cfg, T, device)
+
+
+def mx_linear_forward(cfg: _MxLinearCfg, x: MxMatrix, w: MxMatrix, y: torch.Tensor,
+                      ws: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                      residual: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_mx_linear_forward: y = residual + act(x w^T + bias)."""
+    T, K, N, dt = _need(y, "y").shape[0], cfg.in_dim, cfg.out_dim, _TORCH_DT[cfg.dtype]
+    _call("moe_mx_linear_forward", cfg, T, _Mx(*_mx(x, "x", T, K, cfg.format)),
+          _Mx(*_mx(w, "w", N, K, 1)), _packed(bias, "bias", dt, N),
+          *_rows(residual, "residual", dt, T, N), *_rows(y, "y", dt, T, N), *_ws(ws), _queue(stream))
+
+
+def make_mx_ffn_cfg(hidden: int, inter: int, act: str = "silu", dtype=BF16,
+                    form: str = "e4m3") -> _MxFfnCfg:
+    """moe_mx_ffn_cfg; dtype of residual and y, form of x and of the block's middle."""
+    return _MxFfnCfg(hidden, inter, _ACT.get(act, act), _DT_NAME.get(dtype, dtype),
+                     _MX_FORM.get(form, form))
+
+
+def mx_ffn_workspace_bytes(cfg: _MxFfnCfg, T: int) -> int:
+    return int(lib().moe_mx_ffn_workspace_bytes(ctypes.byref(cfg), int(T)))
+
+
+def alloc_mx_ffn_workspace(cfg: _MxFfnCfg, T: int, device="cuda") -> torch.Tensor:
+    return _alloc("mx_ffn", cfg, T, device)
+
+
+def mx_ffn_forward(cfg: _MxFfnCfg, x: MxMatrix, weights: Dict[str, MxMatrix], y: torch.Tensor,
+                   ws: torch.Tensor, residual: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_mx_ffn_forward: y = residual + m w_down^T, m = act(x w_gate^T) * (x w_up^T) in x's form."""
+    T, H, I, dt = _need(y, "y").shape[0], cfg.hidden, cfg.inter, _TORCH_DT[cfg.dtype]
+    _call("moe_mx_ffn_forward", cfg, T, _Mx(*_mx(x, "x", T, H, cfg.format)),
+          _Mx(*_mx(weights.get("w_gate"), "w_gate", I, H, 1)),
+          _Mx(*_mx(weights.get("w_up"), "w_up", I, H, 1)),
+          _Mx(*_mx(weights.get("w_down"), "w_down", H, I, 1)),
+          *_rows(residual, "residual", dt, T, H), *_rows(y, "y", dt, T, H), *_ws(ws), _queue(stream))

@@ -208,6 +208,7 @@ struct NormArgs {
   const void *residual, *branch, *du, *dh;
   const void *w_post, *b_post, *w_pre, *b_pre, *gate;
   void *u, *h;                       // forward outputs
+  uint8_t *codes, *scales;           // h in microscaled form (mx.h)
   void *d_residual, *d_branch;       // backward outputs
   void *dw_post, *db_post, *dw_pre, *db_pre, *dgate;
   float* part;                       // [4][workgroups][H]: sums of dw_post, db_post, dw_pre, db_pre
@@ -219,7 +220,7 @@ struct NormArgs {
   float eps, scale;
 };
 int norm_backward_workers(int64_t T, int H);
-hipError_t launch_norm_forward(const NormArgs& a, bool bf16, hipStream_t st);
+hipError_t launch_norm_forward(const NormArgs& a, bool bf16, hipStream_t st, int form = 0);  // form: of codes
 hipError_t launch_norm_backward(const NormArgs& a, bool bf16, hipStream_t st);
 constexpr int kNormMaxHidden = 16384;
 

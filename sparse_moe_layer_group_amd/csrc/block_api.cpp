@@ -4,59 +4,15 @@
 // dense_gemm.hip.
 #include <hip/hip_runtime.h>
 
-#include <atomic>
 #include <cmath>
-#include <cstring>
 
-#include "../../include/moe.h"
-#include "block.h"
+#include "block_checks.h"
+#include "mx.h"
 
 namespace {
 
 using moe::bf16_t;
-
-constexpr int64_t kMaxRows = int64_t(1) << 24, kMaxLd = int64_t(1) << 22;
-constexpr int32_t kMaxDim = 131072;
-
-#define MOE_TRY(expr)                             \
-  do {                                            \
-    if ((expr) != hipSuccess) return MOE_ERR_HIP; \
-  } while (0)
-
-// the current device is a gfx950 GPU (cached per device)
-int check_device() {
-  static std::atomic<int> state[64];
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return MOE_ERR_HIP;
-  if (dev < 0 || dev >= 64) return MOE_ERR_DEVICE;
-  int st = state[dev].load(std::memory_order_relaxed);
-  if (st == 0) {
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return MOE_ERR_HIP;
-    st = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : -1;
-    state[dev].store(st, std::memory_order_relaxed);
-  }
-  return st == 1 ? MOE_OK : MOE_ERR_DEVICE;
-}
-
-int check_dtype(int32_t dt) { return dt == MOE_F32 || dt == MOE_BF16 ? MOE_OK : MOE_ERR_DTYPE; }
-bool bad_dim(int32_t d) { return d < 1 || d > kMaxDim; }
-bool bad_rows(int64_t T) { return T < 0 || T > kMaxRows; }
-bool bad_ld(const void* p, int64_t ld, int64_t cols) { return p != nullptr && (ld < cols || ld >= kMaxLd); }
-bool bad_ws(const void* ws, size_t have, size_t need) {
-  return need > 0 && (ws == nullptr || have < need || (reinterpret_cast<uintptr_t>(ws) & 15) != 0);
-}
-
-// consecutive pieces of a workspace, 256 bytes apart
-struct Carver {
-  char* base;  // NULL: only the total is wanted
-  size_t used = 0;
-  template <typename P> P* take(size_t bytes) {
-    char* p = base == nullptr ? nullptr : base + used;
-    used += (bytes + 255) & ~size_t(255);
-    return reinterpret_cast<P*>(p);
-  }
-};
+using namespace moe::checks;
 
 // ---------------------------------------------------------------- norm
 
@@ -346,6 +302,31 @@ int moe_norm_forward(const moe_norm_cfg* cfg, int64_t T, const void* residual, i
   a.h = h;
   a.ld_h = ld_h;
   MOE_TRY(moe::launch_norm_forward(a, cfg->dtype == MOE_BF16, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+int moe_norm_mx_forward(const moe_norm_cfg* cfg, int32_t format, int64_t T, const void* residual, int64_t ld_residual,
+                        const void* branch, int64_t ld_branch, const moe_norm_params* params, void* u, int64_t ld_u,
+                        void* h, int64_t ld_h, uint8_t* codes, uint8_t* scales, void* stream) {
+  int rc = validate(cfg, T);
+  if (rc != MOE_OK) return rc;
+  if (check_format(format) != MOE_OK) return MOE_ERR_DTYPE;
+  if (T == 0) return MOE_OK;
+  if (residual == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_NULL;
+  if ((rc = check_params(*cfg, params, branch != nullptr, true)) != MOE_OK) return rc;
+  const int64_t H = cfg->hidden;
+  if (bad_ld(residual, ld_residual, H) || bad_ld(branch, ld_branch, H) || bad_ld(u, ld_u, H) || bad_ld(h, ld_h, H) ||
+      bad_mx(codes, scales))
+    return MOE_ERR_SHAPE;
+  if ((rc = check_device()) != MOE_OK) return rc;
+  moe::NormArgs a = norm_args(*cfg, T, residual, ld_residual, branch, ld_branch, *params);
+  a.u = u;
+  a.ld_u = ld_u;
+  a.h = h;
+  a.ld_h = ld_h;
+  a.codes = codes;
+  a.scales = scales;
+  MOE_TRY(moe::launch_norm_forward(a, cfg->dtype == MOE_BF16, static_cast<hipStream_t>(stream), format));
   return MOE_OK;
 }
 

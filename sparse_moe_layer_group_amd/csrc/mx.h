@@ -1,0 +1,157 @@
+// Microscaled operands (mx_quant.hip, mx_stream.hip, mx_gemm.hip, norm_kernels.hip,
+// mx_api.cpp); not part of the C ABI.
+//
+// Blocks of 32 consecutive elements of a row share a power of two, kept as its
+// exponent's byte e + 127 (255: NaN): value = element 2^e, elements E4M3 or E2M1.
+// Rows are padded to 128 elements, one step of the matrix instructions: codes
+// of padding are 0, a row of codes takes 128 or 64 bytes a step and its scales 4.
+#pragma once
+
+#include "block.h"
+
+namespace moe {
+
+// codes of enum moe_mx_format
+constexpr int kMxE4M3 = 0, kMxE2M1 = 1;
+
+inline int64_t mx_steps(int64_t cols) { return (cols + 127) / 128; }
+constexpr int mx_step_bytes(int form) { return form == kMxE4M3 ? 128 : 64; }
+
+// ---------------------------------------------------------------- codes
+
+// exponent of the largest element
+template <int FORM> struct MxForm {
+  static constexpr int EMAX = FORM == kMxE4M3 ? 8 : 2;
+  static constexpr float MOST = FORM == kMxE4M3 ? 448.f : 6.f;
+  static constexpr int WORDS = FORM == kMxE4M3 ? 2 : 1;  // of 8 codes
+};
+
+// magnitude bits, in whose order NaN and infinity come last
+MOE_DEV uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Scale byte of a block from its largest magnitude's bits: floor(log2) - EMAX,
+// not below 2^-127 (a block of zeros has that one), NaN for NaN and infinity.
+template <int FORM> MOE_DEV uint32_t mx_scale_byte(uint32_t most) {
+  const int field = int(most >> 23);
+  return field == 255 ? 255u : uint32_t(field > MxForm<FORM>::EMAX ? field - MxForm<FORM>::EMAX : 0);
+}
+// 2^-e of a scale byte (at most 2^127, exact); a NaN's is 0
+MOE_DEV float mx_inverse(uint32_t byte) { return byte == 255u ? 0.f : __uint_as_float((254u - byte) << 23); }
+// 2^e of a scale byte
+MOE_DEV float mx_power(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7fc00000u : byte == 0u ? 0x00400000u : byte << 23);
+}
+
+// Codes of 8 elements, the first in the low bits: v 2^-e rounded to nearest
+// even, saturated (amax 2^-e is below twice the largest element).  The products
+// with a power of two are exact, so codes depend on v alone.
+template <int FORM> MOE_DEV void mx_encode8(const float (&v)[8], uint32_t byte, uint32_t (&o)[MxForm<FORM>::WORDS]) {
+  constexpr float M = MxForm<FORM>::MOST;
+  const float inv = mx_inverse(byte);
+  float s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = byte == 255u ? 0.f : __builtin_amdgcn_fmed3f(v[i] * inv, -M, M);
+  if constexpr (FORM == kMxE4M3) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      int p = __builtin_amdgcn_cvt_pk_fp8_f32(s[4 * h], s[4 * h + 1], 0, false);
+      o[h] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(s[4 * h + 2], s[4 * h + 3], p, true));
+    }
+  } else {
+    uint32_t p = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, s[0], s[1], 1.0f, 0);
+    p = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p, s[2], s[3], 1.0f, 1);
+    p = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p, s[4], s[5], 1.0f, 2);
+    o[0] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p, s[6], s[7], 1.0f, 3);
+  }
+}
+template <int FORM> MOE_DEV uint32_t mx_encode1(float v, uint32_t byte) {
+  constexpr float M = MxForm<FORM>::MOST;
+  const float s = byte == 255u ? 0.f : __builtin_amdgcn_fmed3f(v * mx_inverse(byte), -M, M);
+  if constexpr (FORM == kMxE4M3) return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(s, s, 0, false)) & 255u;
+  else return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, s, s, 1.0f, 0) & 15u;
+}
+
+// the larger of this and another lane's (a move within 16-lane rows)
+template <int CTRL> MOE_DEV uint32_t max_dpp(uint32_t v) {
+  return max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), CTRL, 0xf, 0xf, true)));
+}
+// scale byte of the block that a quad of lanes has, 8 elements each
+template <int FORM> MOE_DEV uint32_t mx_quad_scale(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, magnitude(v[i]));
+  m = max_dpp<0xb1>(m);  // lane ^ 1
+  m = max_dpp<0x4e>(m);  // lane ^ 2
+  return mx_scale_byte<FORM>(m);
+}
+
+// ---------------------------------------------------------------- products
+
+// The matrix instruction adds a block's products in groups of 8, in 8 bits each
+// cut off 13 bits below the power of two of its group's largest; then the four
+// blocks' sums and the accumulator, cut off 23 bits or so below the largest.
+// (Measured: with 256 and w = 1 in a group 2^-5 counts and 2^-6 does not.)
+// Products of 4-bit elements, 0.25 to 36, all count.  Those of 8 bits leave
+// sums that are off by 1e-5 to 2e-5 of their size on normal values: far below
+// what bfloat16 outputs show, but not what float32 ones should.  Their elements
+// are then taken in three parts, one instruction each, within which nothing is
+// cut off: |v| >= 8, 2^-4 <= |v| < 8 and below (products with 4-bit elements of
+// 6 to 0.5: powers 11 to -1, 5 to -8, -2 to -10).
+MOE_DEV uint32_t bytes_from(uint32_t c, uint32_t least) {  // 255 in bytes whose magnitude is >= least (two digits)
+  const uint32_t m = ((c & 0x7f7f7f7fu) + (0x80u - least) * 0x01010101u) & 0x80808080u;
+  return (m - (m >> 7)) | m;
+}
+template <int PART> MOE_DEV i32x4 mx_part(i32x4 c) {
+  i32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v = uint32_t(c[i]);
+    const uint32_t in = PART == 0 ? bytes_from(v, 0x50u) : PART == 1 ? bytes_from(v, 0x18u) & ~bytes_from(v, 0x50u)
+                                                                     : ~bytes_from(v, 0x18u);
+    o[i] = int(v & in);
+  }
+  return o;
+}
+
+// acc + w x of one step: w 16 rows of 4-bit codes, x 16 of FORM (E4M3: chunks
+// lo and hi of 16 bytes, in `exact` parts, the smallest first)
+template <int FORM, bool EXACT>
+MOE_DEV f32x4 mx_multiply(i32x4 w, int sw, i32x4 lo, i32x4 hi, int sx, f32x4 acc) {
+  const i32x8 a = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
+  auto add = [&](i32x4 l, i32x4 h) {
+    const i32x8 b = __builtin_shufflevector(l, h, 0, 1, 2, 3, 4, 5, 6, 7);
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, FORM == kMxE4M3 ? 0 : 4, 0, sw, 0, sx);
+  };
+  if constexpr (FORM == kMxE4M3 && EXACT) {
+    add(mx_part<2>(lo), mx_part<2>(hi));
+    add(mx_part<1>(lo), mx_part<1>(hi));
+    add(mx_part<0>(lo), mx_part<0>(hi));
+  } else {
+    add(lo, hi);
+  }
+  return acc;
+}
+
+// ---------------------------------------------------------------- launchers
+
+// x [rows][cols] of f32 or bfloat16, rows ld apart, to codes and scales, and back
+hipError_t launch_mx_quantize(int form, bool f32, const void* x, int64_t ld, int64_t rows, int cols, uint8_t* codes,
+                              uint8_t* scales, hipStream_t st);
+hipError_t launch_mx_dequantize(int form, bool f32, const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
+                                void* y, int64_t ld, hipStream_t st);
+
+// out = residual + act(x w^T + bias), or with w2 the quantised act(x w^T) * (x w2^T);
+// w and w2 are E2M1, x of either form; T token rows, N weight rows, `steps` of 128.
+struct MxArgs {
+  const uint8_t *x, *sx, *w, *sw, *w2, *sw2;
+  const void *bias, *residual;
+  void* out;
+  int64_t ld_residual, ld_out;
+  float* mid;  // w2: the products' product, [T][ld_out]
+  int64_t T;
+  int N, steps, act, f32;
+  int exact;   // E4M3: block sums of float32's precision (mx_multiply)
+};
+hipError_t launch_mx_stream(const MxArgs& a, int form, hipStream_t st);
+
+}  // namespace moe

@@ -46,7 +46,7 @@
 // us, the time that one wave takes for its row or two.  Of the backward's 80 us
 // the sums' barriers and the column gradients' arithmetic are what is above the
 // copy's 70.
-#include "block.h"
+#include "mx.h"
 
 namespace moe {
 
@@ -252,11 +252,53 @@ template <typename TE_, int NV_, bool ONE_WAVE_, bool LAYER_, bool WHOLE_> struc
 };
 
 // NormArgs::options, set by the launchers from the pointers given
-constexpr int kNormPost = 1, kNormGate = 2, kNormU = 4, kNormPre = 8, kNormDResidual = 16, kNormDBranch = 32;
+constexpr int kNormPost = 1, kNormGate = 2, kNormU = 4, kNormPre = 8, kNormDResidual = 16, kNormDBranch = 32,
+              kNormH = 64;
 
 int norm_options(const NormArgs& a) {
   return (a.branch && a.w_post ? kNormPost : 0) | (a.gate_rows ? kNormGate : 0) | (a.u ? kNormU : 0) |
-         (a.h || a.dh ? kNormPre : 0) | (a.d_residual ? kNormDResidual : 0) | (a.d_branch ? kNormDBranch : 0);
+         (a.h || a.dh || a.codes ? kNormPre : 0) | (a.d_residual ? kNormDResidual : 0) |
+         (a.d_branch ? kNormDBranch : 0) | (a.h ? kNormH : 0);
+}
+
+// ---------------------------------------------------------------- microscaled output
+
+// Vector j of a row as codes and scales.  WHOLE: a quad of lanes has a block, and
+// each lane the codes of 8 elements in a row.  Else an element's block is that of
+// 32 lanes; of 4-bit codes every other lane stores its own and its neighbour's.
+template <int FORM, bool WHOLE>
+MOE_DEV void put_mx(uint8_t* codes, uint8_t* scales, const Cols<WHOLE>& c, int j, float (&v)[8]) {
+  const int end = (c.H + 127) & ~127;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = c.in(j, i) ? v[i] : 0.f;
+  if constexpr (WHOLE) {
+    const uint32_t byte = mx_quad_scale<FORM>(v);
+    constexpr int W = MxForm<FORM>::WORDS;
+    uint32_t o[W];
+    mx_encode8<FORM>(v, byte, o);
+    const int col = c.at(j, 0);
+    if (col >= end) return;
+    if constexpr (W == 2) *reinterpret_cast<uint2*>(codes + col) = uint2{o[0], o[1]};
+    else *reinterpret_cast<uint32_t*>(codes + col / 2) = o[0];
+    if ((c.tid & 3) == 0) scales[col / 32] = uint8_t(byte);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t m = magnitude(v[i]);
+      m = max_dpp<0xb1>(m);
+      m = max_dpp<0x4e>(m);
+      m = max_dpp<0x124>(m);
+      m = max_dpp<0x128>(m);
+      m = max(m, uint32_t(__shfl_xor(int(m), 16, 64)));
+      const uint32_t byte = mx_scale_byte<FORM>(m), code = mx_encode1<FORM>(v[i], byte);
+      const uint32_t next = uint32_t(__builtin_amdgcn_mov_dpp(int(code), 0xb1, 0xf, 0xf, true));
+      const int col = c.at(j, i);
+      if (col >= end) continue;
+      if (FORM == kMxE4M3) codes[col] = uint8_t(code);
+      else if ((c.tid & 1) == 0) codes[col / 2] = uint8_t(code | next << 4);
+      if ((c.tid & 31) == 0) scales[col / 32] = uint8_t(byte);
+    }
+  }
 }
 
 constexpr int kRowThreads = 512;  // most threads of a workgroup that shares a row
@@ -266,7 +308,8 @@ constexpr int kRowWaves = 4;  // waves (one row each) of a workgroup of one-wave
 
 // ---------------------------------------------------------------- forward
 
-template <class S>
+// FORM: of the microscaled output, or -1 (none)
+template <class S, int FORM>
 __global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kRowThreads) void norm_forward_kernel(NormArgs a) {
   typedef typename S::TE TE;
   constexpr int NV = S::NV;
@@ -303,6 +346,9 @@ __global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kRowThreads) void no
   if (f) f += t0 * a.ld_branch;
   TE* u_row = static_cast<TE*>(a.u) + (a.u ? t0 * a.ld_u : 0);
   TE* h_row = static_cast<TE*>(a.h) + (a.h ? t0 * a.ld_h : 0);
+  const int64_t ld_codes = int64_t((H + 127) / 128) * (FORM == kMxE2M1 ? 64 : 128), ld_scales = (H + 127) / 128 * 4;
+  uint8_t* code_row = FORM < 0 ? nullptr : a.codes + t0 * ld_codes;
+  uint8_t* scale_row = FORM < 0 ? nullptr : a.scales + t0 * ld_scales;
   auto fetch = [&]() {  // the next row
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -353,11 +399,16 @@ __global__ __launch_bounds__(S::ONE_WAVE ? 64 * kRowWaves : kRowThreads) void no
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         affine<S>(u[j], wpre[j], bpre[S::LAYER ? j : 0]);
-        put(h_row, c, j, u[j]);
+        if (FORM < 0 || (opt & kNormH)) put(h_row, c, j, u[j]);
+        if constexpr (FORM >= 0) put_mx<FORM>(code_row, scale_row, c, j, u[j]);
       }
     }
     if (a.u) u_row += a.ld_u;
     if (a.h) h_row += a.ld_h;
+    if (FORM >= 0) {
+      code_row += ld_codes;
+      scale_row += ld_scales;
+    }
   }
 }
 
@@ -731,10 +782,10 @@ template <class F, typename TE> void pick_shape(const NormArgs& a, const NormPla
   else pick_form<F, TE, 4, false>(a, f);
 }
 
-template <typename TE>
+template <typename TE, int FORM>
 hipError_t launch_forward(const NormArgs& a, const NormPlan& p, unsigned grid, hipStream_t st) {
   auto f = [&](auto shape) {
-    hipLaunchKernelGGL((norm_forward_kernel<decltype(shape)>), dim3(grid), dim3(p.threads), 0, st, a);
+    hipLaunchKernelGGL((norm_forward_kernel<decltype(shape), FORM>), dim3(grid), dim3(p.threads), 0, st, a);
   };
   pick_shape<decltype(f), TE>(a, p, f);
   return hipGetLastError();
@@ -769,7 +820,7 @@ int norm_backward_workers(int64_t T, int H) {
   return int(T < most ? T : most);
 }
 
-hipError_t launch_norm_forward(const NormArgs& args, bool bf16, hipStream_t st) {
+hipError_t launch_norm_forward(const NormArgs& args, bool bf16, hipStream_t st, int form) {
   NormArgs a = args;
   a.options = norm_options(a);
   const NormPlan p = norm_plan(a.H);
@@ -777,7 +828,10 @@ hipError_t launch_norm_forward(const NormArgs& args, bool bf16, hipStream_t st) 
   const int64_t most = p.one_wave ? 256 * 32 : 256 * (2048 / p.threads);
   a.workers = int(a.T < most ? a.T : most);
   const unsigned grid = unsigned(p.one_wave ? (a.workers + kRowWaves - 1) / kRowWaves : a.workers);
-  return bf16 ? launch_forward<bf16_t>(a, p, grid, st) : launch_forward<float>(a, p, grid, st);
+  if (!a.codes) return bf16 ? launch_forward<bf16_t, -1>(a, p, grid, st) : launch_forward<float, -1>(a, p, grid, st);
+  if (form == kMxE4M3)
+    return bf16 ? launch_forward<bf16_t, kMxE4M3>(a, p, grid, st) : launch_forward<float, kMxE4M3>(a, p, grid, st);
+  return bf16 ? launch_forward<bf16_t, kMxE2M1>(a, p, grid, st) : launch_forward<float, kMxE2M1>(a, p, grid, st);
 }
 
 hipError_t launch_norm_backward(const NormArgs& args, bool bf16, hipStream_t st) {
