@@ -13,7 +13,7 @@ LIB = os.path.join(HERE, "libmoe_mi355x.so")
 SOURCES = ["moe_api.cpp", "route_kernels.hip", "gemm_kernels.hip", "stream_gemm.hip", "tile_gemm.hip",
            "fp8_kernels.hip", "balance_kernels.hip", "bwd_kernels.hip", "bwd_fp8_kernels.hip",
            "block_api.cpp", "norm_kernels.hip", "dense_gemm.hip", "dense_stream.hip",
-           "mx_api.cpp", "mx_quant.hip", "mx_stream.hip"]
+           "mx_api.cpp", "mx_quant.hip", "mx_stream.hip", "mx_gemm.hip"]
 ARCH = "gfx950"
 
 # Packed fp32 instructions are disabled for all device code.

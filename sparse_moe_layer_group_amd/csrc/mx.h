@@ -115,12 +115,12 @@ template <int PART> MOE_DEV i32x4 mx_part(i32x4 c) {
 
 // acc + w x of one step: w 16 rows of 4-bit codes, x 16 of FORM (E4M3: chunks
 // lo and hi of 16 bytes, in `exact` parts, the smallest first)
-template <int FORM, bool EXACT>
+template <int FORM, bool EXACT, int BYTE = 0>
 MOE_DEV f32x4 mx_multiply(i32x4 w, int sw, i32x4 lo, i32x4 hi, int sx, f32x4 acc) {
   const i32x8 a = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
   auto add = [&](i32x4 l, i32x4 h) {
     const i32x8 b = __builtin_shufflevector(l, h, 0, 1, 2, 3, 4, 5, 6, 7);
-    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, FORM == kMxE4M3 ? 0 : 4, 0, sw, 0, sx);
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, FORM == kMxE4M3 ? 0 : 4, BYTE, sw, BYTE, sx);
   };
   if constexpr (FORM == kMxE4M3 && EXACT) {
     add(mx_part<2>(lo), mx_part<2>(hi));
@@ -140,18 +140,26 @@ hipError_t launch_mx_quantize(int form, bool f32, const void* x, int64_t ld, int
 hipError_t launch_mx_dequantize(int form, bool f32, const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
                                 void* y, int64_t ld, hipStream_t st);
 
-// out = residual + act(x w^T + bias), or with w2 the quantised act(x w^T) * (x w2^T);
-// w and w2 are E2M1, x of either form; T token rows, N weight rows, `steps` of 128.
+// out = residual + act(x w^T + bias), or with w2 act(x w^T) * (x w2^T), by tiles as
+// codes and scales of x's form, from the stream in float32; w and w2 are E2M1, x of either form; T token rows, N
+// weight rows, `steps` of 128.
 struct MxArgs {
   const uint8_t *x, *sx, *w, *sw, *w2, *sw2;
-  const void *bias, *residual;
-  void* out;
-  int64_t ld_residual, ld_out;
-  float* mid;  // w2: the products' product, [T][ld_out]
+  DenseEpi epi;              // kEpiOut; w2: its act and N
+  uint8_t *codes, *scales;   // w2, tiles
+  const float* middle;       // stream: x in float32, quantised as it is read, [T][steps * 128]
+  float* mid;                // w2, stream: float32, [T][padded N], zeros from N
   int64_t T;
-  int N, steps, act, f32;
-  int exact;   // E4M3: block sums of float32's precision (mx_multiply)
+  int N, steps;
+  int split, steps_per_split;  // (set by the launcher) the contraction's parts
+  float* part;                 // (set by the launcher) split > 1: [split][w2 ? 2 : 1][T][ld_part]
+  int64_t ld_part;
+  int exact;                 // E4M3: block sums of float32's precision (mx_multiply)
 };
+constexpr int kMxStreamTokens = 16;
 hipError_t launch_mx_stream(const MxArgs& a, int form, hipStream_t st);
+// part: mx_part_bytes of room
+size_t mx_part_bytes(int64_t T, int N, bool dual);
+hipError_t launch_mx_gemm(const MxArgs& a, int form, float* part, hipStream_t st);
 
 }  // namespace moe

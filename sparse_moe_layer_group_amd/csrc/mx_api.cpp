@@ -3,6 +3,8 @@
 // layout and launch order.  The norm with a microscaled output is in block_api.cpp.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "block_checks.h"
 #include "mx.h"
 
@@ -31,30 +33,48 @@ int validate(const moe_mx_ffn_cfg* c, int64_t T) {
   return MOE_OK;
 }
 
-size_t linear_carve(void* ws) {
+// Room for the parts of split contractions: of T tokens' and every smaller batch's
+struct LinearWork {
+  float* part;
+  size_t bytes;
+};
+LinearWork linear_carve(const moe_mx_linear_cfg& c, int64_t T, void* ws) {
   Carver v{static_cast<char*>(ws)};
-  v.take<char>(1);  // a size that is not 0, which a query has for what is invalid
-  return v.used;
+  LinearWork L{};
+  L.part = v.take<float>(T > moe::kMxStreamTokens ? moe::mx_part_bytes(T, c.out_dim, false) : 1);
+  L.bytes = v.used;
+  return L;
 }
 
+// Few tokens: whether the middle is quantised by a launch of its own, and not by the
+// down projection's workgroups, each for itself as it reads it.  That launch costs 3
+// us, as much as a wave's quantising of four steps (hidden 2048, a call, one and 16
+// tokens: inter 4096 13.3 and 16.9 us inside, 16.4 and 16.5 apart; 7168 17.2 and
+// 26.7, 16.4 and 19.6).
+bool quantises_apart(int inter) { return moe::mx_steps(inter) > 32; }
+
 struct FfnWork {
-  float* mid;
-  uint8_t *codes, *scales;
+  float* mid;               // few tokens: the middle
+  uint8_t *codes, *scales;  // and quantised
+  float* part;
   size_t bytes;
 };
 FfnWork ffn_carve(const moe_mx_ffn_cfg& c, int64_t T, void* ws) {
   Carver v{static_cast<char*>(ws)};
   FfnWork F{};
+  const bool few = T <= moe::kMxStreamTokens;
+  const size_t mid = size_t(std::min<int64_t>(T, moe::kMxStreamTokens)) * size_t(moe::mx_steps(c.inter)) * 128 * sizeof(float);
   F.codes = v.take<uint8_t>(moe_mx_code_bytes(c.format, T, c.inter));
   F.scales = v.take<uint8_t>(moe_mx_scale_bytes(T, c.inter));
-  F.mid = v.take<float>(size_t(T) * size_t(c.inter) * sizeof(float));
+  const size_t parts = std::max(moe::mx_part_bytes(T, c.inter, true), moe::mx_part_bytes(T, c.hidden, false));
+  F.part = v.take<float>(few ? mid : std::max(mid, parts));
+  F.mid = F.part;
   F.bytes = v.used;
   return F;
 }
 
 moe::MxArgs product(int64_t T, int N, int K, const moe_mx* x, const moe_mx* w, int act, bool f32) {
   moe::MxArgs a{};
-  a.exact = f32;  // (of 8-bit codes)
   a.x = x->codes;
   a.sx = x->scales;
   a.w = w->codes;
@@ -62,9 +82,20 @@ moe::MxArgs product(int64_t T, int N, int K, const moe_mx* x, const moe_mx* w, i
   a.T = T;
   a.N = N;
   a.steps = int(moe::mx_steps(K));
-  a.act = act;
-  a.f32 = f32;
+  a.exact = f32;
+  a.epi.mode = moe::kEpiOut;
+  a.epi.act = act;
+  a.epi.f32 = f32;
+  a.epi.M = T;
+  a.epi.N = N;
   return a;
+}
+void output(moe::MxArgs& a, const void* bias, const void* residual, int64_t ld_residual, void* y, int64_t ld_y) {
+  a.epi.bias = bias;
+  a.epi.residual = residual;
+  a.epi.ld_residual = ld_residual;
+  a.epi.out = y;
+  a.epi.ld_out = ld_y;
 }
 
 int check_operands(const moe_mx* const* m, int count) {
@@ -117,7 +148,7 @@ int moe_mx_dequantize(int32_t format, int32_t dtype, int64_t rows, int32_t cols,
 
 size_t moe_mx_linear_workspace_bytes(const moe_mx_linear_cfg* cfg, int64_t T) {
   if (validate(cfg, T) != MOE_OK || T == 0) return 0;
-  return linear_carve(nullptr);
+  return linear_carve(*cfg, T, nullptr).bytes;
 }
 
 int moe_mx_linear_forward(const moe_mx_linear_cfg* cfg, int64_t T, const moe_mx* x, const moe_mx* w, const void* bias,
@@ -130,15 +161,14 @@ int moe_mx_linear_forward(const moe_mx_linear_cfg* cfg, int64_t T, const moe_mx*
   if ((rc = check_operands(m, 2)) != MOE_OK) return rc;
   const int N = cfg->out_dim;
   if (bad_ld(residual, ld_residual, N) || bad_ld(y, ld_y, N)) return MOE_ERR_SHAPE;
-  if (bad_ws(ws, ws_bytes, linear_carve(ws))) return MOE_ERR_WORKSPACE;
+  const LinearWork L = linear_carve(*cfg, T, ws);
+  if (bad_ws(ws, ws_bytes, L.bytes)) return MOE_ERR_WORKSPACE;
   if ((rc = check_device()) != MOE_OK) return rc;
   moe::MxArgs a = product(T, N, cfg->in_dim, x, w, cfg->act, cfg->dtype == MOE_F32);
-  a.bias = bias;
-  a.residual = residual;
-  a.ld_residual = ld_residual;
-  a.out = y;
-  a.ld_out = ld_y;
-  MOE_TRY(moe::launch_mx_stream(a, cfg->format, static_cast<hipStream_t>(stream)));
+  output(a, bias, residual, ld_residual, y, ld_y);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  MOE_TRY(T <= moe::kMxStreamTokens ? moe::launch_mx_stream(a, cfg->format, st)
+                                    : moe::launch_mx_gemm(a, cfg->format, L.part, st));
   return MOE_OK;
 }
 
@@ -166,17 +196,24 @@ int moe_mx_ffn_forward(const moe_mx_ffn_cfg* cfg, int64_t T, const moe_mx* x, co
   moe::MxArgs up = product(T, I, H, x, w_gate, cfg->act, cfg->dtype == MOE_F32);
   up.w2 = w_up->codes;
   up.sw2 = w_up->scales;
-  up.mid = F.mid;
-  up.ld_out = I;
-  MOE_TRY(moe::launch_mx_stream(up, cfg->format, st));
-  MOE_TRY(moe::launch_mx_quantize(cfg->format, true, F.mid, I, T, I, F.codes, F.scales, st));
+  const bool few = T <= moe::kMxStreamTokens;
   const moe_mx mid{F.codes, F.scales};
   moe::MxArgs down = product(T, H, I, &mid, w_down, MOE_ACT_NONE, cfg->dtype == MOE_F32);
-  down.residual = residual;
-  down.ld_residual = ld_residual;
-  down.out = y;
-  down.ld_out = ld_y;
-  MOE_TRY(moe::launch_mx_stream(down, cfg->format, st));
+  output(down, nullptr, residual, ld_residual, y, ld_y);
+  if (few) {
+    up.mid = F.mid;
+    MOE_TRY(moe::launch_mx_stream(up, cfg->format, st));
+    if (quantises_apart(I))
+      MOE_TRY(moe::launch_mx_quantize(cfg->format, true, F.mid, moe::mx_steps(I) * 128, T, I, F.codes, F.scales, st));
+    else
+      down.middle = F.mid;
+    MOE_TRY(moe::launch_mx_stream(down, cfg->format, st));
+  } else {
+    up.codes = F.codes;
+    up.scales = F.scales;
+    MOE_TRY(moe::launch_mx_gemm(up, cfg->format, F.part, st));
+    MOE_TRY(moe::launch_mx_gemm(down, cfg->format, F.part, st));
+  }
   return MOE_OK;
 }
 

@@ -273,6 +273,39 @@ def test_linear(T, K, N, pad, dtype, form):
         assert _pads_kept(y)
 
 
+# products large enough for every tile, and contractions that are split: whole and ragged tiles, with
+# residuals that the largest tile can copy as they lie (rows of whole 16 bytes) and cannot
+LARGE = [(130, 4100, 40, 0, 0), (200, 130, 4100, 3, 0), (333, 7168, 512, 0, 0), (700, 2050, 3000, 5, 0),
+         (1100, 1500, 2048, 0, 0), (3000, 2600, 4100, 0, 0), (2816, 2600, 4352, 0, 8), (2817, 2304, 4353, 1, 1),
+         (4096, 2304, 4096, 0, 0)]
+
+
+def _on_gpu(v):
+    return None if v is None else v.detach().to(DEV, F64)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("T,K,N,pad,pad_residual", LARGE)
+def test_linear_large(T, K, N, pad, pad_residual, form):
+    x, xv = _matrix(T, K, form, 1)
+    w, wv = _matrix(N, K, "e2m1", 2, K ** -0.5)
+    xg, wg = _on_gpu(xv), _on_gpu(wv)
+    for i, (dtype, act, bias, res) in enumerate((("bf16", "none", False, True), ("bf16", "silu", True, False),
+                                                 ("f32", "gelu", True, True))):
+        say(f"linear large {form} {dtype} T={T} K={K} N={N} pad={pad} {act}")
+        b = _rand(dtype, N, seed=20 + i) if bias else None
+        r = _rows(dtype, T, N, pad_residual, 30 + i) if res else None
+        cfg = moe.make_mx_linear_cfg(K, N, act, dtype, form)
+        y, ws = _out(dtype, T, N, pad), moe.alloc_mx_linear_workspace(cfg, T, DEV)
+        moe.mx_linear_forward(cfg, x, w, y, ws, bias=b, residual=r)
+        want = M.linear(xg, wg, _on_gpu(b), _on_gpu(r), act).cpu()
+        assert R.worst(y, want) <= M.tolerance(dtype, K, form), (act, R.worst(y, want))
+        assert _pads_kept(y)
+        if res:                                                         # into the residual itself
+            moe.mx_linear_forward(cfg, x, w, r, ws, bias=b, residual=r)
+            assert torch.equal(r, y)
+
+
 def _whole(rows, cols, form, seed, most):
     """Whole numbers up to `most` at scale 1 (their blocks' scales say so where a block holds an element of
     2^emax): sums of their products are exact in float32."""
@@ -357,6 +390,28 @@ FFN = [  # T, hidden, inter, pad
     (1, 1, 1, 0), (1, 256, 512, 0), (2, 1001, 777, 3), (16, 640, 130, 0), (17, 130, 33, 1), (50, 1024, 264, 0),
     (64, 512, 256, 8), (65, 72, 8, 0), (129, 1033, 257, 5), (300, 1024, 256, 0), (520, 384, 1100, 1),
 ]
+
+
+FFN_LARGE = [(200, 2600, 40, 0), (129, 7168, 300, 0), (1500, 1500, 2000, 3), (1500, 2600, 4100, 0), (2049, 2304, 3300, 0),
+             (5, 300, 5000, 0), (16, 2048, 4097, 1)]
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("T,H,I,pad", FFN_LARGE)
+def test_ffn_large(T, H, I, pad, form):
+    say(f"ffn large {form} T={T} H={H} I={I} pad={pad}")
+    x, xv = _matrix(T, H, form, 1)
+    w, wv = _ffn_weights(H, I, 2)
+    g = {k: _on_gpu(v) for k, v in wv.items()}
+    for dtype in TYPES:
+        r = _rows(dtype, T, H, pad, 30)
+        cfg = moe.make_mx_ffn_cfg(H, I, "silu", dtype, form)
+        y, ws = _out(dtype, T, H, pad), moe.alloc_mx_ffn_workspace(cfg, T, DEV)
+        moe.mx_ffn_forward(cfg, x, w, y, ws, residual=r)
+        mid = R.act("silu", _on_gpu(xv) @ g["w_gate"].T) * (_on_gpu(xv) @ g["w_up"].T)
+        want = (_on_gpu(M.rounded(mid.cpu(), form)) @ g["w_down"].T).cpu() + _lift(r)
+        assert R.worst(y, want) <= M.tolerance(dtype, I, form) + M.flips(dtype, H, form), R.worst(y, want)
+        assert _pads_kept(y)
 
 
 def _ffn_weights(H, I, seed):
