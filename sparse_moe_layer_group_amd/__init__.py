@@ -713,12 +713,17 @@ def _mx(m: Optional[MxMatrix], name: str, rows: int, cols: int, form: int):
     """(codes, scales) pointers of a matrix of this size and form."""
     if m is None:
         raise ValueError(f"{name} is required")
-    if m.cols != cols or _MX_FORM.get(m.form) != form:
-        raise ValueError(f"{name}: {m.cols} columns of {m.form}, expected {cols} of "
+    codes, scales, kind, width = m
+    if width != cols or _MX_FORM.get(kind) != form:
+        raise ValueError(f"{name}: {width} columns of {kind}, expected {cols} of "
                          f"{'e4m3' if form == 0 else 'e2m1'}")
     steps = -(-cols // 128)
-    return (_packed(m.codes, f"{name}.codes", torch.uint8, rows, steps * _MX_STEP[form]),
-            _packed(m.scales, f"{name}.scales", torch.uint8, rows, steps * 4))
+    if (codes.shape != (rows, steps * _MX_STEP[form]) or scales.shape != (rows, steps * 4)
+            or codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_cuda
+            or not scales.is_cuda or not codes.is_contiguous() or not scales.is_contiguous()):
+        _packed(codes, f"{name}.codes", torch.uint8, rows, steps * _MX_STEP[form])  # says what is wrong
+        _packed(scales, f"{name}.scales", torch.uint8, rows, steps * 4)
+    return codes.data_ptr(), scales.data_ptr()
 
 
 def _mx_tensor(t: torch.Tensor, name: str) -> int:

@@ -52,8 +52,10 @@ template <int FORM_, int TM_, int TN_, bool DUAL_, bool EXACT_> struct MxShape {
   static constexpr int LDS = STAGES * STAGE + SCALES;
   static_assert(STAGES >= 3 && STAGES * COPIES < 62, "vmcnt has 6 bits");
   static_assert(!DUAL || TN >= 128, "a wave has whole blocks of the product's columns");
-  // a tile's rows of bfloat16 fit the stages (as pairs of rows a copy)
-  static constexpr bool IMAGE = !DUAL && TM == 256 && TN == 256;
+  // a tile's rows of bfloat16 fit the stages, whole 16 of them a stage (smaller tiles
+  // have another workgroup on their CU instead: 8192 x 2048 x 7168 by 128 x 128 143 us,
+  // with the image 165, 45 registers out to memory)
+  static constexpr bool IMAGE = !DUAL && TM * TN > 128 * 128;
   static_assert(!IMAGE || (STAGES * STAGE >= 2 * TM * TN && STAGE % (16 * 2 * TN) == 0 && XS % 1024 == 0));
   // accumulators past what 256 registers hold beside the operands: written as
   // assembly, which updates them where they lie
@@ -121,21 +123,23 @@ template <int FORM> MOE_DEV void mx_gated(const MxArgs& g, int64_t m, int n, flo
 // columns from `col` there): the residual's values, where they are there (joins),
 // give way to the results in their places, and rows of these go out 16 bytes a
 // lane.  m, n: of its first element in the output.
-template <int MB, int NB>
+template <int TN, int MB, int NB>
 MOE_DEV void image_epilogue(const MxArgs& g, lds_u8* image, f32x4 (&acc)[MB][NB], int64_t m, int n, int row, int col,
                             bool joins) {
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+  constexpr int RB = 2 * TN, MASK = RB / 16 < 16 ? RB / 16 - 1 : 15;  // bytes of a row; of the chunks' places
+  constexpr int LPR = 2 * NB, RPI = 64 / LPR;  // lanes of a wave's part of a row, rows at a time
   const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
   float bias[NB][4];
 #pragma unroll
   for (int j = 0; j < NB; ++j)
 #pragma unroll
     for (int v = 0; v < 4; ++v) bias[j][v] = g.epi.bias ? load1(g.epi, g.epi.bias, n + 16 * j + 4 * q + v) : 0.f;
-  lds_u8* mine = image + (row + r16) * 512 + (q & 1) * 8;
+  lds_u8* mine = image + (row + r16) * RB + (q & 1) * 8;
   const int chunk = col / 8 + (q >> 1);
-  auto place = [&](int i, int j) { return (lds_u32x2*)(mine + i * (16 * 512) + ((chunk + 2 * j) ^ r16) * 16); };
-  bf16_t* out = static_cast<bf16_t*>(g.epi.out) + (m + q) * g.epi.ld_out + n + 8 * r16;
+  auto place = [&](int i, int j) { return (lds_u32x2*)(mine + i * (16 * RB) + ((chunk + 2 * j) ^ (r16 & MASK)) * 16); };
+  bf16_t* out = static_cast<bf16_t*>(g.epi.out) + (m + lane / LPR) * g.epi.ld_out + n + 8 * (lane % LPR);
 #pragma unroll 1
   for (int i = 0; i < MB; ++i) {
     f32x4 row16[NB];
@@ -164,12 +168,11 @@ MOE_DEV void image_epilogue(const MxArgs& g, lds_u8* image, f32x4 (&acc)[MB][NB]
         *place(i, j + h) = u32x2{pack_bf16(v[4 * h], v[4 * h + 1]), pack_bf16(v[4 * h + 2], v[4 * h + 3])};
       }
     }
-    // 16 rows of 16 chunks, four rows at a time
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = 16 * i + 4 * k + q;
-      const u32x4 x = *(lds_u32x4*)(image + (row + r) * 512 + ((col / 8 + r16) ^ (r & 15)) * 16);
-      reinterpret_cast<u32x4_at2*>(out + (16 * i + 4 * k) * g.epi.ld_out)->v = x;
+    for (int k = 0; k < 16 / RPI; ++k) {
+      const int r = 16 * i + RPI * k + lane / LPR;
+      const u32x4 x = *(lds_u32x4*)(image + (row + r) * RB + ((col / 8 + lane % LPR) ^ (r & MASK)) * 16);
+      reinterpret_cast<u32x4_at2*>(out + (16 * i + RPI * k) * g.epi.ld_out)->v = x;
     }
   }
 }
@@ -231,11 +234,12 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void mx_gemm_kernel
   __amdgpu_buffer_rsrc_t rx = buffer_rsrc(px, max(all_x, 0)), rw = buffer_rsrc(pw, max(all_w, 0));
 
   // A whole tile of bfloat16 rows goes out through an image of it in LDS, over the
-  // stages: rows of 512 bytes, 16-byte chunk c of row r at c ^ (r & 15).  The
+  // stages: rows of RB bytes, 16-byte chunk c of row r at c ^ (r & MASK).  The
   // residual's tile comes in there by the last STAGES steps' copies, which have
   // no more operands to fetch.
+  constexpr int RB = 2 * TN, MASK = RB / 16 < 16 ? RB / 16 - 1 : 15, IR = 1024 / RB;  // IR: rows of a copy
   const bool whole = m0 + TM <= g.T && (S::DUAL || n0 + NCOL <= g.N);
-  const bool image = S::IMAGE && whole && !g.epi.f32;
+  const bool image = S::IMAGE && whole && !g.epi.f32 && g.split == 1;
   const bf16_t* res = static_cast<const bf16_t*>(g.epi.residual);
   const uint32_t ld_res = uint32_t(g.epi.ld_residual) * 2u;
   const bool joins = image && res != nullptr && g.steps >= S::STAGES && (ld_res & 15) == 0 &&
@@ -244,7 +248,7 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void mx_gemm_kernel
   const int all_res = int((TM - 1) * ld_res) + TN * 2;
   bool tail = false;
   auto take_residual = [&](int stage) __attribute__((always_inline)) {  // the rows whose place this stage is
-    const int skip = stage / (2 * TN) * int(ld_res);
+    const int skip = stage / RB * int(ld_res);
     rx = rw = buffer_rsrc(pres + skip, max(all_res - skip, 0));
   };
   auto enter_tail = [&](int stage) __attribute__((always_inline)) {
@@ -252,8 +256,8 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void mx_gemm_kernel
 #pragma unroll
     for (int i = 0; i < S::XCP + S::WCP; ++i) {
       const int kb = i < S::XCP ? S::XCP * wave + i : S::XS / 1024 + S::WCP * wave + i - S::XCP;
-      const int row = 2 * kb + (lane >> 5);
-      const uint32_t off = row * ld_res + ((lane & 31) ^ (row & 15)) * 16;
+      const int row = IR * kb + lane / (RB / 16);
+      const uint32_t off = row * ld_res + ((lane % (RB / 16)) ^ (row & MASK)) * 16;
       if (i < S::XCP) xoff[i] = off;
       else woff[i - S::XCP] = off;
     }
@@ -447,7 +451,7 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void mx_gemm_kernel
   // accumulator v of lane l is row l % 16, column 4 (l / 16) + v.
   if constexpr (S::IMAGE) {
     if (image && (joins || res == nullptr)) {
-      image_epilogue<MB, NB>(g, lds, acc, m0 + wm * (TM / 2), n0 + wn * (TN / 2), wm * (TM / 2), wn * (TN / 2), joins);
+      image_epilogue<TN, MB, NB>(g, lds, acc, m0 + wm * (TM / 2), n0 + wn * (TN / 2), wm * (TM / 2), wn * (TN / 2), joins);
       return;
     }
   }
@@ -507,15 +511,14 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void mx_gemm_kernel
         *(lds_f32x4*)(rows32 + (16 * (i & 1) + r16) * PITCH + 4 * (16 * j + 4 * q)) = acc[i][j];
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (whole) {
+    if (mrow + 32 <= g.T && (S::DUAL || n0 + wn * OC + OC <= g.N)) {  // (this wave's, in a tile that is not whole too)
 #pragma unroll 1
       for (int r = lane / LPR; r < 32; r += RPI * AHEAD)
         finish(mrow, r, std::true_type{}, std::integral_constant<int, AHEAD>{});
-    } else {
+    } else if (S::DUAL || n < g.N) {
 #pragma unroll 1
       for (int r = lane / LPR; r < 32; r += RPI)
-        if (mrow + r < g.T && (S::DUAL || n < g.N))
-          finish(mrow, r, std::false_type{}, std::integral_constant<int, 1>{});
+        if (mrow + r < g.T) finish(mrow, r, std::false_type{}, std::integral_constant<int, 1>{});
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
@@ -523,9 +526,10 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void mx_gemm_kernel
 
 // Sums of a split contraction, in order, and the epilogue on them: eight columns
 // of a row a lane.
-template <int FORM, bool DUAL> __global__ __launch_bounds__(256) void mx_join_kernel(MxArgs g) {
+constexpr int kJoinThreads = 64;  // (as many workgroups as there are for few rows)
+template <int FORM, bool DUAL> __global__ __launch_bounds__(kJoinThreads) void mx_join_kernel(MxArgs g) {
   const uint32_t pieces = uint32_t(g.ld_part) / 8;  // of a row: whole quads of lanes
-  const uint32_t id = blockIdx.x * 256 + threadIdx.x, row = id / pieces;
+  const uint32_t id = blockIdx.x * kJoinThreads + threadIdx.x, row = id / pieces;
   const int64_t m = row;
   const int n = int(id - row * pieces) * 8;
   if (m >= g.T) return;
@@ -533,7 +537,7 @@ template <int FORM, bool DUAL> __global__ __launch_bounds__(256) void mx_join_ke
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[0][i] = u[0][i] = 0.f;
   const int64_t part = g.T * g.ld_part;
-#pragma unroll 4
+#pragma unroll 8
   for (int s = 0; s < g.split; ++s) {
     const float* p = g.part + s * (DUAL ? 2 : 1) * part + m * g.ld_part + n;
     float x[8], y[8];
@@ -584,8 +588,8 @@ struct TileCost {
 };
 constexpr int kTiles = 4;
 constexpr TileCost kCosts[2][kTiles] = {  // by form
-    {{64, 64, 0.195f, 0.3f}, {64, 128, 0.29f, 0.5f}, {128, 128, 0.46f, 2.f}, {256, 256, 1.32f, 17.f}},
-    {{64, 64, 0.155f, 0.3f}, {64, 128, 0.25f, 0.5f}, {128, 128, 0.39f, 2.f}, {256, 256, 0.92f, 17.f}}};
+    {{64, 64, 0.197f, 0.3f}, {64, 128, 0.292f, 0.6f}, {128, 128, 0.455f, 1.4f}, {256, 256, 1.32f, 17.f}},
+    {{64, 64, 0.158f, 0.3f}, {64, 128, 0.25f, 0.6f}, {128, 128, 0.375f, 1.4f}, {256, 256, 0.92f, 17.f}}};
 constexpr int kMostSplit = 16, kFewest = 3;  // parts, steps of one
 constexpr float kJoin = 4.f, kPartBytes = 3e6f;  // us, bytes a us
 constexpr int kUnits = 256;
@@ -636,9 +640,9 @@ template <int FORM, bool EXACT> hipError_t launch_form(const MxArgs& args, float
       else err = launch_tile<FORM, false, 256, 256>(g, st);
   }
   if (err != hipSuccess || g.split == 1) return err;
-  const unsigned grid = unsigned((g.T * (g.ld_part / 8) + 255) / 256);  // (at most 256 tiles' rows)
-  if (g.w2) hipLaunchKernelGGL((mx_join_kernel<FORM, true>), dim3(grid), dim3(256), 0, st, g);
-  else hipLaunchKernelGGL((mx_join_kernel<FORM, false>), dim3(grid), dim3(256), 0, st, g);
+  const unsigned grid = unsigned((g.T * (g.ld_part / 8) + kJoinThreads - 1) / kJoinThreads);  // (at most 256 tiles' rows)
+  if (g.w2) hipLaunchKernelGGL((mx_join_kernel<FORM, true>), dim3(grid), dim3(kJoinThreads), 0, st, g);
+  else hipLaunchKernelGGL((mx_join_kernel<FORM, false>), dim3(grid), dim3(kJoinThreads), 0, st, g);
   return hipGetLastError();
 }
 
