@@ -7,6 +7,8 @@
 // consecutive elements (one or two 16-byte loads), a quad of lanes a block, so
 // the largest magnitude takes two lane moves; a workgroup's lanes lie along a row
 // as far as it goes, then over rows.
+#include <algorithm>
+
 #include "mx.h"
 
 namespace moe {
@@ -79,46 +81,54 @@ __global__ __launch_bounds__(kLanes) void mx_dequantize_kernel(const uint8_t* co
 
 namespace {
 
-unsigned grid_of(int64_t rows, int cols, int lx) {
-  const int64_t across = (mx_steps(cols) * 16 + lx - 1) / lx, down = (rows + kLanes / lx - 1) / (kLanes / lx);
-  return unsigned(across * down);  // (rows <= 2^24, cols <= 2^17: at most 2^30)
-}
-template <typename TE> hipError_t quantize(int form, const void* x, int64_t ld, int64_t rows, int cols, uint8_t* codes,
-                                           uint8_t* scales, hipStream_t st) {
-  const int lx = lane_columns(cols);
-  const dim3 grid(grid_of(rows, cols, lx));
-  const TE* p = static_cast<const TE*>(x);
-  if (form == kMxE4M3) {
-    hipLaunchKernelGGL((mx_quantize_kernel<TE, kMxE4M3>), grid, dim3(kLanes), 0, st, p, ld, rows, cols, lx, codes, scales);
-  } else {
-    hipLaunchKernelGGL((mx_quantize_kernel<TE, kMxE2M1>), grid, dim3(kLanes), 0, st, p, ld, rows, cols, lx, codes, scales);
+// Rows of a launch: a grid has less than 2^32 threads.
+constexpr int64_t kMostGroups = int64_t(1) << 23;
+template <class F> hipError_t by_rows(int64_t rows, int cols, F launch) {
+  const int lx = lane_columns(cols), down = kLanes / lx;
+  const int64_t across = (mx_steps(cols) * 16 + lx - 1) / lx, most = kMostGroups / across * down;
+  for (int64_t first = 0; first < rows; first += most) {
+    const int64_t n = std::min(most, rows - first);
+    launch(first, n, lx, dim3(unsigned(across * ((n + down - 1) / down))));
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
   }
-  return hipGetLastError();
+  return hipSuccess;
 }
-template <typename TE> hipError_t dequantize(int form, const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
-                                             void* y, int64_t ld, hipStream_t st) {
-  const int lx = lane_columns(cols);
-  const dim3 grid(grid_of(rows, cols, lx));
-  TE* p = static_cast<TE*>(y);
-  if (form == kMxE4M3) {
-    hipLaunchKernelGGL((mx_dequantize_kernel<TE, kMxE4M3>), grid, dim3(kLanes), 0, st, codes, scales, rows, cols, lx, p, ld);
-  } else {
-    hipLaunchKernelGGL((mx_dequantize_kernel<TE, kMxE2M1>), grid, dim3(kLanes), 0, st, codes, scales, rows, cols, lx, p, ld);
-  }
-  return hipGetLastError();
+template <typename TE, int FORM> hipError_t quantize(const void* x, int64_t ld, int64_t rows, int cols, uint8_t* codes,
+                                                     uint8_t* scales, hipStream_t st) {
+  const int64_t steps = mx_steps(cols);
+  return by_rows(rows, cols, [&](int64_t first, int64_t n, int lx, dim3 grid) {
+    hipLaunchKernelGGL((mx_quantize_kernel<TE, FORM>), grid, dim3(kLanes), 0, st, static_cast<const TE*>(x) + first * ld,
+                       ld, n, cols, lx, codes + first * steps * mx_step_bytes(FORM), scales + first * steps * 4);
+  });
+}
+template <typename TE, int FORM> hipError_t dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                                       int cols, void* y, int64_t ld, hipStream_t st) {
+  const int64_t steps = mx_steps(cols);
+  return by_rows(rows, cols, [&](int64_t first, int64_t n, int lx, dim3 grid) {
+    hipLaunchKernelGGL((mx_dequantize_kernel<TE, FORM>), grid, dim3(kLanes), 0, st,
+                       codes + first * steps * mx_step_bytes(FORM), scales + first * steps * 4, n, cols, lx,
+                       static_cast<TE*>(y) + first * ld, ld);
+  });
 }
 
 }  // namespace
 
 hipError_t launch_mx_quantize(int form, bool f32, const void* x, int64_t ld, int64_t rows, int cols, uint8_t* codes,
                               uint8_t* scales, hipStream_t st) {
-  return f32 ? quantize<float>(form, x, ld, rows, cols, codes, scales, st)
-             : quantize<bf16_t>(form, x, ld, rows, cols, codes, scales, st);
+  if (form == kMxE4M3)
+    return f32 ? quantize<float, kMxE4M3>(x, ld, rows, cols, codes, scales, st)
+               : quantize<bf16_t, kMxE4M3>(x, ld, rows, cols, codes, scales, st);
+  return f32 ? quantize<float, kMxE2M1>(x, ld, rows, cols, codes, scales, st)
+             : quantize<bf16_t, kMxE2M1>(x, ld, rows, cols, codes, scales, st);
 }
 hipError_t launch_mx_dequantize(int form, bool f32, const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
                                 void* y, int64_t ld, hipStream_t st) {
-  return f32 ? dequantize<float>(form, codes, scales, rows, cols, y, ld, st)
-             : dequantize<bf16_t>(form, codes, scales, rows, cols, y, ld, st);
+  if (form == kMxE4M3)
+    return f32 ? dequantize<float, kMxE4M3>(codes, scales, rows, cols, y, ld, st)
+               : dequantize<bf16_t, kMxE4M3>(codes, scales, rows, cols, y, ld, st);
+  return f32 ? dequantize<float, kMxE2M1>(codes, scales, rows, cols, y, ld, st)
+             : dequantize<bf16_t, kMxE2M1>(codes, scales, rows, cols, y, ld, st);
 }
 
 }  // namespace moe

@@ -557,3 +557,110 @@ def test_no_tokens():
         moe.norm_mx_forward(moe.make_norm_cfg(64), y, y, {"w_pre": _rand("bf16", 64)}, y, x)
         moe.mx_linear_forward(lcfg, x, w["w_gate"], y, moe.alloc_mx_linear_workspace(lcfg, 0, DEV))
         moe.mx_ffn_forward(fcfg, x, w, y, moe.alloc_mx_ffn_workspace(fcfg, 0, DEV))
+
+
+# ---------------------------------------------------------------- past 32 bits
+
+def _tiled(base, times):
+    return base.expand(times, *base.shape).reshape(times * base.shape[0], -1)
+
+
+def test_more_threads_than_a_grid_has():
+    rows, times, cols = 1024, 1 << 14, 1032                             # a workgroup a row, 2^24 of them
+    base = _rand("bf16", rows, cols, seed=5)
+    small = Guarded(rows, cols, "e2m1")
+    moe.mx_quantize(base, small.m)
+    values = _out("bf16", rows, cols)
+    moe.mx_dequantize(small.m, values)
+    x = _tiled(base, times)
+    out = moe.alloc_mx(rows * times, cols, "e2m1", DEV)
+    out.codes.fill_(0xa5)
+    moe.mx_quantize(x, out)
+    assert bool((out.codes.view(times, rows, -1) == small.m.codes).all())
+    assert bool((out.scales.view(times, rows, -1) == small.m.scales).all())
+    x.zero_()
+    moe.mx_dequantize(out, x)
+    assert bool((x.view(times, rows, cols) == values).all())
+    del x, out
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_offsets_past_32_bits(form):
+    big = 16 if form == "e4m3" else 4
+    # an output of 2.4e9 elements
+    (x, xv), (w, wv) = _whole(1000, 128, form, 1, big), _whole(4100, 128, "e2m1", 2, 4)
+    cfg = moe.make_mx_linear_cfg(128, 4100, "none", "bf16", form)
+    full = moe.MxMatrix(_tiled(x.codes, 600), _tiled(x.scales, 600), form, 128)
+    y = _out("bf16", 600000, 4100)
+    moe.mx_linear_forward(cfg, full, w, y, moe.alloc_mx_linear_workspace(cfg, 600000, DEV))
+    assert bool((y.view(600, 1000, 4100) == (xv @ wv.T).bfloat16().to(DEV)).all())
+    del y, full
+    # operands of 5e9 bytes
+    T = 40000 if form == "e4m3" else 80000
+    (x, xv), (w, wv) = _whole(100, 131072, form, 1, 4), _whole(24, 131072, "e2m1", 2, 4)
+    cfg = moe.make_mx_linear_cfg(131072, 24, "none", "f32", form)
+    full = moe.MxMatrix(_tiled(x.codes, T // 100), _tiled(x.scales, T // 100), form, 131072)
+    y = _out("f32", T, 24)
+    moe.mx_linear_forward(cfg, full, w, y, moe.alloc_mx_linear_workspace(cfg, T, DEV))
+    assert bool((y.view(T // 100, 100, 24) == (xv @ wv.T).float().to(DEV)).all())
+    del y, full
+    # a middle, and a norm's output, of 5e9 elements
+    (x, _), (w, _) = _whole(1000, 128, form, 1, big), _ffn_weights(128, 16384, 2)
+    cfg = moe.make_mx_ffn_cfg(128, 16384, "silu", "bf16", form)
+    full = moe.MxMatrix(_tiled(x.codes, 300), _tiled(x.scales, 300), form, 128)
+    y = _out("bf16", 300000, 128)
+    moe.mx_ffn_forward(cfg, full, w, y, moe.alloc_mx_ffn_workspace(cfg, 300000, DEV))
+    assert bool((y.view(300, 1000, 128) == y[:1000]).all()) and bool(torch.isfinite(y[:1000]).all())
+    r, params = _rand("bf16", 1000, 16384, seed=3), {"w_pre": _rand("bf16", 16384, seed=4)}
+    cfg, small = moe.make_norm_cfg(16384), moe.alloc_mx(1000, 16384, form, DEV)
+    moe.norm_mx_forward(cfg, r, None, params, None, small)
+    out = moe.alloc_mx(300000, 16384, form, DEV)
+    moe.norm_mx_forward(cfg, _tiled(r, 300), None, params, None, out)
+    assert bool((out.codes.view(300, 1000, -1) == small.codes).all())
+    assert bool((out.scales.view(300, 1000, -1) == small.scales).all())
+    del out, y, full
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_two_streams_at_once(form):
+    # each with a workspace of its own, the operands shared
+    T, H, I = 80, 1500, 700
+    x, _ = _matrix(T, H, form, 1)
+    w, _ = _ffn_weights(H, I, 2)
+    cfg = moe.make_mx_ffn_cfg(H, I, "silu", "bf16", form)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [moe.alloc_mx_ffn_workspace(cfg, T, DEV) for _ in range(3)]
+    y = [_out("bf16", T, H) for _ in range(3)]
+    moe.mx_ffn_forward(cfg, x, w, y[2], ws[2])
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for k, s in enumerate(streams):
+            moe.mx_ffn_forward(cfg, x, w, y[k], ws[k], stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(y[0], y[2]) and torch.equal(y[1], y[2])
+
+
+def test_two_graphs_share_a_workspace():
+    # replayed one after the other on a stream, as calls that share a workspace are ordered
+    H, I, form = 640, 300, "e4m3"
+    w, _ = _ffn_weights(H, I, 2)
+    cfg = moe.make_mx_ffn_cfg(H, I, "silu", "bf16", form)
+    ws = moe.alloc_mx_ffn_workspace(cfg, 300, DEV)
+    runs = []
+    for T in (300, 9):
+        x, _ = _matrix(T, H, form, T)
+        y, want = _out("bf16", T, H), _out("bf16", T, H)
+        moe.mx_ffn_forward(cfg, x, w, want, ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            moe.mx_ffn_forward(cfg, x, w, y, ws)
+        runs.append((g, x, y, want))
+    for _ in range(3):
+        for g, _, y, _ in runs:
+            y.fill_(77)
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, want) for _, _, y, want in runs)
