@@ -141,8 +141,8 @@ hipError_t launch_mx_dequantize(int form, bool f32, const uint8_t* codes, const 
                                 void* y, int64_t ld, hipStream_t st);
 
 // out = residual + act(x w^T + bias), or with w2 act(x w^T) * (x w2^T), by tiles as
-// codes and scales of x's form, from the stream in float32; w and w2 are E2M1, x of either form; T token rows, N
-// weight rows, `steps` of 128.
+// codes and scales of x's form, from the stream in float32; w and w2 are E2M1, x of
+// either form; T token rows, N weight rows, `steps` of 128.
 struct MxArgs {
   const uint8_t *x, *sx, *w, *sw, *w2, *sw2;
   DenseEpi epi;              // kEpiOut; w2: its act and N

@@ -3,8 +3,9 @@
 //
 //   out = residual + act(x w^T + bias), or the quantised act(x w^T) * (x w2^T)
 //
-// Bound by the matrix cores: a v_mfma_scale_f32_16x16x128_f8f6f4 of 4-bit
-// operands takes 16 cycles, with an 8-bit one 32.  Workgroup tile TM x TN, four
+// Bound by the matrix cores and the copies that feed them: a
+// v_mfma_scale_f32_16x16x128_f8f6f4 of 4-bit operands takes 16 cycles, with an 8-bit
+// one 32; alone they reach 6.7 and 4.4 PFLOP/s here.  Workgroup tile TM x TN, four
 // waves in 2 x 2, the contraction in steps of 128 (one instruction's) through a
 // ring of LDS stages filled by buffer_load ... lds copies.  A wave keeps a step's
 // operands in registers and reads the next step's while it multiplies: a row
@@ -23,6 +24,18 @@
 // tile's last row, so rows past the end read as zero; rows are whole steps.
 // Copies of steps past the last read what follows there, or zeros, and are not
 // used.
+//
+// Measured (tokens x in x out, a call): 8192 x 7168 x 7168 with a residual, 8-bit
+// tokens 336 us (2.5 PFLOP/s), 4-bit 274 (3.1); 8192 x 7168 x 2048 93 and 69; 8192 x
+// 2048 x 7168 142 and 126, of which the residual, 117 MB, is 20.  A 256 x 256 tile's
+// step takes 1.32 and 0.92 us; without its copies 1.06 and 0.69, without its LDS reads
+// too 0.97 and 0.62, the instructions' own time at the clock that this load leaves.
+// Matrix cores busy by counters: gate and up of 8192 tokens 59% of the time, 4096 x
+// 7168 x 7168 49% (448 tiles, 1.75 turns of the chip), 8192 x 7168 x 2048 in 4 bits
+// 29%, with 17 us of prologue and epilogue to a single turn of 52.
+// Measured and not kept: copies staggered over the waves or issued early in a step
+// (equal or slower), eight stages (no change), waves in two groups that split the
+// contraction (no gain), 32x32x64 instructions (no faster).
 #include <type_traits>
 
 #include "dense_tiles.h"
@@ -581,7 +594,13 @@ template <int FORM, bool EXACT, int TM, int TN> hipError_t launch_tile(const MxA
 
 // A product's tile and split of the contraction, by their time in us: turns of the
 // chip, each of so many steps and what a tile takes beside them; a second launch
-// that joins the parts, and these through memory.
+// that joins the parts, and these through memory.  Calls measured with every tile
+// forced (64 x 64, 64 x 128, 128 x 128, 256 x 256, each with the best split), 8-bit
+// tokens: 50 x 7168 x 2048 10.8, 11.3, 11.6, 70.5 (not split 14.3); 333 x 7168 x 7168
+// 33.1, 31.0, 28.1, 76.2; 1024 x 7168 x 2048 25.8, 21.1, 27.2, 75.1; 2048 x 7168 x 7168
+// 167, 127, 108, 84.2; 4096 x 7168 x 2048 94.0, 72.6, 59.0, 77.5.  Of 13 sizes and both
+// forms the rule took the fastest or one within 3% of it, but for 50 x 7168 x 7168 in
+// 4 bits (14.2 by 64 x 64, 12.9 by 64 x 128).
 struct TileCost {
   int tm, tn;  // token rows, weight rows
   float step, rest;

@@ -19,6 +19,12 @@
 // it reads, in every workgroup again, to the codes that mx_quant.hip would write.
 // (32 columns a workgroup, which quantises them: 64 workgroups for a block of hidden
 // 7168 and inter 2048, one token, 13 to 16 us.)
+//
+// Measured, one token of 8 bits: 7168 -> 7168 8.9 us (27 MB of weights, 3.1 TB/s, which
+// counts 3 us of a launch), gate and up of 7168 -> 2048 6.0 (15.6 MB), down from there
+// with the middle's quantising 7.0 (7.8 MB).  An instruction is full at 16 tokens, so
+// that is the most: calls of 16 here and 17 by tiles, 7168 -> 7168 12.7 and 12.0 us (4
+// bits 9.7 and 13.4), 7168 -> 2048 8.2 and 11.0, the block of these 19.2 and 19.0.
 #include "dense_tiles.h"
 #include "mx.h"
 
