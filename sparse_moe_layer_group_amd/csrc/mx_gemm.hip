@@ -16,9 +16,10 @@
 //
 // Stages.  Rows of 128 bytes (8 bits): 16-byte chunk c of row r at c ^ (r & 7).
 // Rows of 64 (4 bits): two to a line of 128, chunk c of row r at
-// (4 (r & 1) + c) ^ (r / 2 & 7).  Neither has bank conflicts.  Scales come four
-// steps at a time, 16 bytes a row, and are turned about in LDS so that a lane reads
-// a word with its block's of all four.
+// (4 (r & 1) + c) ^ (r / 2 & 7).  The 16 lanes of a read's turn then have all banks
+// once (counted with scales, copies and the epilogue, conflicts are 9 to 13% of the
+// LDS's cycles).  Scales come four steps at a time, 16 bytes a row, and are turned
+// about in LDS so that a lane reads a word with its block's of all four.
 //
 // Bounds.  A resource starts at the step's own first byte and ends with the
 // tile's last row, so rows past the end read as zero; rows are whole steps.
