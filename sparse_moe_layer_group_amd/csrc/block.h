@@ -128,19 +128,24 @@ MOE_DEV u32x4 pack8(const float (&v)[8]) {
   return u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
 }
 
-template <bool WHOLE> MOE_DEV void store8(float* row, int c, int n, const float (&v)[8]) {
+// STREAM: past the caches, for what is not read again soon
+template <bool STREAM, class T, class V> MOE_DEV void put_vector(T* p, V v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, &p->v);
+  else p->v = v;
+}
+template <bool WHOLE, bool STREAM = false> MOE_DEV void store8(float* row, int c, int n, const float (&v)[8]) {
   if (c + 8 <= n) {
-    reinterpret_cast<f32x4_at4*>(row + c)->v = f32x4{v[0], v[1], v[2], v[3]};
-    reinterpret_cast<f32x4_at4*>(row + c + 4)->v = f32x4{v[4], v[5], v[6], v[7]};
+    put_vector<STREAM>(reinterpret_cast<f32x4_at4*>(row + c), f32x4{v[0], v[1], v[2], v[3]});
+    put_vector<STREAM>(reinterpret_cast<f32x4_at4*>(row + c + 4), f32x4{v[4], v[5], v[6], v[7]});
   } else if (!WHOLE) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (c + i < n) row[c + i] = v[i];
   }
 }
-template <bool WHOLE> MOE_DEV void store8(bf16_t* row, int c, int n, const float (&v)[8]) {
+template <bool WHOLE, bool STREAM = false> MOE_DEV void store8(bf16_t* row, int c, int n, const float (&v)[8]) {
   if (c + 8 <= n) {
-    reinterpret_cast<u32x4_at2*>(row + c)->v = pack8(v);
+    put_vector<STREAM>(reinterpret_cast<u32x4_at2*>(row + c), pack8(v));
   } else if (!WHOLE) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)

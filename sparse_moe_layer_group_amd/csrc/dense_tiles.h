@@ -79,8 +79,8 @@ template <int MODE, bool INSIDE> MOE_DEV void load_bias(const DenseEpi& e, int n
 // memory operations, the stores too, before the next rows.)  early: the rows of
 // the residual or upstream gradient, where they were loaded before.  total:
 // kEpiActBack's results are added to it, as they are before they are rounded,
-// and left in v.
-template <int MODE, bool INSIDE, bool RESIDUAL, int R>
+// and left in v.  STREAM: kEpiOut's rows go past the caches.
+template <int MODE, bool INSIDE, bool RESIDUAL, int R, bool STREAM = false>
 MOE_DEV void dense_rows(const DenseEpi& e, int64_t m, int step, int n, float (&v)[R][8], float (&u)[R][8],
                         const float (&b)[1][8], float (&total)[8], const u32x4* early = nullptr) {
   float x[R][8];  // residual, upstream gradient or gate projection
@@ -130,10 +130,10 @@ MOE_DEV void dense_rows(const DenseEpi& e, int64_t m, int step, int n, float (&v
     const int64_t first = m * e.ld_out, next = step * e.ld_out;
     if (e.f32) {
 #pragma unroll
-      for (int k = 0; k < R; ++k) store8<INSIDE>(static_cast<float*>(e.out) + (first + k * next), n, end, v[k]);
+      for (int k = 0; k < R; ++k) store8<INSIDE, STREAM>(static_cast<float*>(e.out) + (first + k * next), n, end, v[k]);
     } else {
 #pragma unroll
-      for (int k = 0; k < R; ++k) store8<INSIDE>(static_cast<bf16_t*>(e.out) + (first + k * next), n, end, v[k]);
+      for (int k = 0; k < R; ++k) store8<INSIDE, STREAM>(static_cast<bf16_t*>(e.out) + (first + k * next), n, end, v[k]);
     }
     return;
   }
@@ -174,11 +174,11 @@ MOE_DEV void dense_rows(const DenseEpi& e, int64_t m, int step, int n, float (&v
   }
 }
 
-template <int MODE, bool INSIDE, int R>
+template <int MODE, bool INSIDE, int R, bool STREAM = false>
 MOE_DEV void dense_epilogue(const DenseEpi& e, int64_t m, int step, int n, float (&v)[R][8], float (&u)[R][8],
                             const float (&b)[1][8], float (&total)[8]) {
-  if (MODE == kEpiOut && e.residual) dense_rows<MODE, INSIDE, true, R>(e, m, step, n, v, u, b, total);
-  else dense_rows<MODE, INSIDE, false, R>(e, m, step, n, v, u, b, total);
+  if (MODE == kEpiOut && e.residual) dense_rows<MODE, INSIDE, true, R, STREAM>(e, m, step, n, v, u, b, total);
+  else dense_rows<MODE, INSIDE, false, R, STREAM>(e, m, step, n, v, u, b, total);
 }
 
 // one element of a matrix of the call's type

@@ -17,7 +17,7 @@
 // Stages.  Rows of 128 bytes (8 bits): 16-byte chunk c of row r at c ^ (r & 7).
 // Rows of 64 (4 bits): two to a line of 128, chunk c of row r at
 // (4 (r & 1) + c) ^ (r / 2 & 7).  The 16 lanes of a read's turn then have all banks
-// once (counted with scales, copies and the epilogue, conflicts are 9 to 13% of the
+// once (counted with scales, copies and the epilogue, conflicts are 9 to 15% of the
 // LDS's cycles).  Scales come four steps at a time, 16 bytes a row, and are turned
 // about in LDS so that a lane reads a word with its block's of all four.
 //
@@ -26,14 +26,19 @@
 // Copies of steps past the last read what follows there, or zeros, and are not
 // used.
 //
+// Outputs are stored past the caches, which then keep the operands for the tiles to
+// come: 4096 x 7168 x 7168 175 -> 162 us, in 4 bits 140 -> 121, 8192 x 7168 x 2048 in 4
+// bits 73 -> 65.  (The residual copied past them too: 132 instead of 124 with 4 bits.)
+//
 // Measured (tokens x in x out, a call): 8192 x 7168 x 7168 with a residual, 8-bit
-// tokens 336 us (2.5 PFLOP/s), 4-bit 274 (3.1); 8192 x 7168 x 2048 93 and 69; 8192 x
-// 2048 x 7168 142 and 126, of which the residual, 117 MB, is 20.  A 256 x 256 tile's
-// step takes 1.32 and 0.92 us; without its copies 1.06 and 0.69, without its LDS reads
-// too 0.97 and 0.62, the instructions' own time at the clock that this load leaves.
-// Matrix cores busy by counters: gate and up of 8192 tokens 59% of the time, 4096 x
-// 7168 x 7168 49% (448 tiles, 1.75 turns of the chip), 8192 x 7168 x 2048 in 4 bits
-// 29%, with 17 us of prologue and epilogue to a single turn of 52.
+// tokens 330 us (2.6 PFLOP/s), 4-bit 258 (3.3); 8192 x 7168 x 2048 85 to 94 and 65; 8192 x
+// 2048 x 7168 127 to 136 and 103 to 116, of which the residual, 117 MB, is 20.  A 256 x
+// 256 tile's step takes 1.32 and 0.92 us; without its copies 1.06 and 0.69, without its
+// LDS reads too 0.97 and 0.62, the instructions' own time at the clock that this load
+// leaves.  Matrix cores busy by counters: gate and up of 8192 tokens 59% of the time,
+// 4096 x 7168 x 7168 51% (448 tiles, 1.75 turns of the chip), 8192 x 7168 x 2048 in 4
+// bits 30%, a single turn of 52 us in the loop and some 12 beside it, and what bias,
+// residual and output take.
 // Measured and not kept: copies staggered over the waves or issued early in a step
 // (equal or slower), eight stages (no change), waves in two groups that split the
 // contraction (no gain), 32x32x64 instructions (no faster).
@@ -186,7 +191,7 @@ MOE_DEV void image_epilogue(const MxArgs& g, lds_u8* image, f32x4 (&acc)[MB][NB]
     for (int k = 0; k < 16 / RPI; ++k) {
       const int r = 16 * i + RPI * k + lane / LPR;
       const u32x4 x = *(lds_u32x4*)(image + (row + r) * RB + ((col / 8 + lane % LPR) ^ (r & MASK)) * 16);
-      reinterpret_cast<u32x4_at2*>(out + (16 * i + RPI * k) * g.epi.ld_out)->v = x;
+      put_vector<true>(reinterpret_cast<u32x4_at2*>(out + (16 * i + RPI * k) * g.epi.ld_out), x);
     }
   }
 }
@@ -507,7 +512,7 @@ template <class S> __global__ __launch_bounds__(kThreads, 1) void mx_gemm_kernel
 #pragma unroll
       for (int k = 0; k < R; ++k) mx_gated<S::FORM>(g, mrow + r + k * RPI, n, v[k], u[k]);
     } else {
-      dense_epilogue<kEpiOut, decltype(inside)::value, R>(g.epi, mrow + r, RPI, n, v, u, bias, total);
+      dense_epilogue<kEpiOut, decltype(inside)::value, R, true>(g.epi, mrow + r, RPI, n, v, u, bias, total);
     }
   };
   // rows at a time where all are inside
@@ -597,19 +602,20 @@ template <int FORM, bool EXACT, int TM, int TN> hipError_t launch_tile(const MxA
 // chip, each of so many steps and what a tile takes beside them; a second launch
 // that joins the parts, and these through memory.  Calls measured with every tile
 // forced (64 x 64, 64 x 128, 128 x 128, 256 x 256, each with the best split), 8-bit
-// tokens: 50 x 7168 x 2048 10.8, 11.3, 11.6, 70.5 (not split 14.3); 333 x 7168 x 7168
-// 33.1, 31.0, 28.1, 76.2; 1024 x 7168 x 2048 25.8, 21.1, 27.2, 75.1; 2048 x 7168 x 7168
-// 167, 127, 108, 84.2; 4096 x 7168 x 2048 94.0, 72.6, 59.0, 77.5.  Of 13 sizes and both
+// tokens: 50 x 7168 x 2048 10.7, 10.7, 11.6, 70.4 (not split 14.3); 333 x 7168 x 7168
+// 32.9, 30.7, 28.0, 76.0; 1024 x 7168 x 2048 25.6, 21.2, 27.5, 75.4; 2048 x 7168 x 7168
+// 163, 123, 104, 81.1; 4096 x 7168 x 2048 93.8, 72.4, 57.7, 76.0; 8192 x 2048 x 7168 210,
+// 168, 145, 136; 8192 x 1024 x 7168 128 x 128 80.7, 256 x 256 89.9.  Of 15 sizes and both
 // forms the rule took the fastest or one within 3% of it, but for 50 x 7168 x 7168 in
-// 4 bits (14.2 by 64 x 64, 12.9 by 64 x 128).
+// 4 bits (14.2 by 64 x 64, 13.3 by 64 x 128).
 struct TileCost {
   int tm, tn;  // token rows, weight rows
   float step, rest;
 };
 constexpr int kTiles = 4;
 constexpr TileCost kCosts[2][kTiles] = {  // by form
-    {{64, 64, 0.197f, 0.3f}, {64, 128, 0.292f, 0.6f}, {128, 128, 0.455f, 1.4f}, {256, 256, 1.32f, 17.f}},
-    {{64, 64, 0.158f, 0.3f}, {64, 128, 0.25f, 0.6f}, {128, 128, 0.375f, 1.4f}, {256, 256, 0.92f, 17.f}}};
+    {{64, 64, 0.197f, 0.3f}, {64, 128, 0.292f, 0.6f}, {128, 128, 0.455f, 2.2f}, {256, 256, 1.32f, 12.f}},
+    {{64, 64, 0.158f, 0.3f}, {64, 128, 0.25f, 0.6f}, {128, 128, 0.375f, 2.f}, {256, 256, 0.92f, 12.f}}};
 constexpr int kMostSplit = 16, kFewest = 3;  // parts, steps of one
 constexpr float kJoin = 4.f, kPartBytes = 3e6f;  // us, bytes a us
 constexpr int kUnits = 256;
