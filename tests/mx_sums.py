@@ -61,10 +61,11 @@ def weights(N, K, seed):
     return torch.where((at < 2)[None], _pairs(gen, N, K), rest)
 
 
-def block(H, I, seed):
+def block(H, I, seed, alone=False):
     """Weights of a gated block for `tokens`, K = H >= 8: row j of the gate takes one element (a large one
     for the first two of every eight j) and that of the up projection ONE, so with relu the middle is on
-    codes (scale 2^-6) and is `tokens`-like itself; `weights` bring it down."""
+    codes (scale 2^-6) and is `tokens`-like itself; `weights` bring it down.  alone: no pair is beside ONE, so
+    one instruction has the up projection's sums too, and some of the gate's."""
     gen = torch.Generator().manual_seed(seed)
     gate, up = _pairs(gen, I, H), _pairs(gen, I, H)
     groups, at = H // 8, torch.arange(I) % 8
@@ -74,7 +75,10 @@ def block(H, I, seed):
     large = at < 2
     gate[rows[large], k[large]], gate[rows[large], k[large] + 1] = 1.0, 0.0
     gate[rows[~large], other[~large]] = 1.0
-    up[rows, torch.randint(0, groups, (I,), generator=gen) * 8 + 2] = 1.0
+    k = torch.randint(0, groups, (I,), generator=gen) * 8
+    up[rows, k + 2] = 1.0
+    if alone:
+        up[rows, k] = up[rows, k + 1] = 0.0
     if H % 8 == 1:
         gate[:, -1] = up[:, -1] = 0.0
     down = weights(H, I, seed + 1)
@@ -83,43 +87,50 @@ def block(H, I, seed):
     return {"w_gate": gate, "w_up": up, "w_down": down}
 
 
-def one_instruction(x, w):
-    """x w^T as one instruction for every step adds it up: of each group of 8, products cut off 13 bits below
-    the power of two of the largest."""
+def _groups(x, w):
+    """Products of E4M3 and E2M1 elements by groups of 8, [T][N][groups][8], and what a group's are cut off
+    at: 2^-13 of the largest power of two, that of an element being its exponent's (the least there is, -6 and
+    0, for the ones below it), of the products that are not zero."""
     pad = -x.shape[1] % 8
     x, w = (torch.nn.functional.pad(t, (0, pad)) for t in (x, w))
     p = (x[:, None] * w[None]).view(x.shape[0], w.shape[0], -1, 8)
-    step = torch.exp2(torch.frexp(p.abs().amax(-1, keepdim=True)).exponent.to(F64) - 1 - 13)
-    return (torch.trunc(p / step) * step).sum((-1, -2))
+    power = (torch.frexp(x).exponent - 1).clamp(min=-6)[:, None] + (torch.frexp(w).exponent - 1).clamp(min=0)[None]
+    most = torch.where(p != 0, power.view(p.shape), -99).amax(-1, keepdim=True)
+    return p, torch.exp2(most.to(F64) - 13)
+
+
+def one_instruction(x, w, scale=None):
+    """x w^T as one instruction for every step adds up elements: of each group of 8, products cut off towards
+    zero; scale: of each element's block of x, [T][K]."""
+    p, step = _groups(x, w)
+    sums = (torch.trunc(p / step) * step).sum(-1)
+    return (sums if scale is None else sums * scale[:, None, ::8]).sum(-1)
 
 
 def lost(x, w):
-    """Bound on what one instruction a step loses of x w^T: seven of each eight products (one is the largest),
-    each by less than 2^-13 of the largest."""
-    pad = -x.shape[1] % 8
-    x, w = (torch.nn.functional.pad(t, (0, pad)) for t in (x, w))
-    most = (x[:, None] * w[None]).abs().view(x.shape[0], w.shape[0], -1, 8).amax(-1)
-    return 7 * 2.0 ** -13 * most.sum(-1)
+    """Bound on what one instruction a step loses of x w^T: of seven of each eight products (the one of the
+    largest power loses nothing) less than a step.  Products are multiples of 2^-10, so what loses has a largest
+    power of 4 at least, its element of x is none of the smallest and its product at least 2^-1 of that power
+    (weights of 0.5): less than 7 * 2^-12 of the largest product."""
+    p, step = _groups(x, w)
+    assert (7 * step <= 7 * 2.0 ** -12 * p.abs().amax(-1, keepdim=True)).logical_or(step <= 2.0 ** -10).all()
+    return 7 * torch.where(step > 2.0 ** -10, step, 0.0).sum((-1, -2))
 
 
-def three_parts(x, w):
+def three_parts(x, w, scale=None):
     """The elements of x in three parts by magnitude, an instruction each."""
     a = x.abs()
-    return sum(one_instruction(torch.where(part, x, 0.0), w) for part in (a < 2.0 ** -4, (a >= 2.0 ** -4) & (a < 8), a >= 8))
+    return sum(one_instruction(torch.where(part, x, 0.0), w, scale)
+               for part in (a < 2.0 ** -4, (a >= 2.0 ** -4) & (a < 8), a >= 8))
+
+
+def exact(x, w, scale=None):
+    return (x if scale is None else x * scale) @ w.T
 
 
 def through(x, w, product):
-    """The gated block (relu) with `product` for the sums, and the middle in E4M3."""
+    """The gated block (relu) with `product` for its sums: the middle, and what comes down from it in E4M3."""
     mid = torch.relu(product(x, w["w_gate"])) * product(x, w["w_up"])
     c, s = M.quantize(mid, "e4m3")
-    # (elements are taken apart without their scale)
     scale = torch.exp2(s.to(F64) - 127).repeat_interleave(32, 1)[:, : mid.shape[1]]
-    kept = M.values(c, s, "e4m3", mid.shape[1])
-    if product is exact:
-        return mid, kept @ w["w_down"].T
-    assert (scale == scale[:, :1]).all()
-    return mid, product(kept / scale, w["w_down"]) * scale[:, :1]
-
-
-def exact(x, w):
-    return x @ w.T
+    return mid, product(M.values(c, s, "e4m3", mid.shape[1]) / scale, w["w_down"], scale)

@@ -1,6 +1,6 @@
 """Sums of 8-bit products on the GPU, with inputs whose sums show what a matrix instruction leaves out
 (tests/mx_sums.py): float32 outputs of projections and blocks have to be equal, at every way that a product
-takes."""
+takes; bfloat16 outputs are within the bounds that the header states."""
 import pytest
 import torch
 
@@ -71,3 +71,53 @@ def test_any_elements_of_a_group(T):
     off = 3 * (4 * 2.0 ** -22 + 2.0 ** -24) * (x.abs() @ w.abs().T)
     assert ((_linear(x, w, "f32").double() - S.exact(x, w)).abs() <= off).all()
     assert ((S.one_instruction(x, w) - S.exact(x, w)).abs() > off).double().mean() > 0.2
+
+
+# What bfloat16 outputs' products lose is what the instruction is stated to keep, no more and no less
+@pytest.mark.parametrize("T,K,N", [(1, 128, 16), (2, 9, 5), (5, 999, 70), (16, 640, 64), (17, 130, 33), (40, 1500, 100),
+                                   (50, 2000, 130), (129, 264, 65), (300, 136, 256)])
+def test_bfloat16_projections_lose_what_is_stated(T, K, N):
+    say(f"stated sums T={T} K={K} N={N}")
+    x, w = S.tokens(T, K, 1), S.weights(N, K, 2)
+    y = _linear(x, w, "bf16")
+    for t in range(T):
+        want = S.one_instruction(x[t:t + 1], w)[0]
+        assert torch.equal(y[t], want.to(torch.bfloat16)), t
+        assert ((want - S.exact(x[t:t + 1], w)[0]).abs() <= S.lost(x[t:t + 1], w)[0]).all()
+
+
+@pytest.mark.parametrize("T", [16, 300])
+def test_any_elements_in_one_instruction(T):
+    # a pair of any large elements that cancels, and any others; one group of eight, so its sum is one float32
+    g = torch.Generator().manual_seed(6)
+    x, w = ((v * (1 - 2 * torch.randint(0, 2, v.shape, generator=g))) for v in
+            (S._pick(g, [e for e in M.GRID["e4m3"] if e < 0.25], T, 8), S._pick(g, M.GRID["e2m1"], 200, 8)))
+    x[:, 0] = x[:, 1] = S._pick(g, [e for e in M.GRID["e4m3"] if e >= 64], T)
+    w[:, 0] = -w[:, 1]
+    want = S.one_instruction(x, w)
+    assert torch.equal(_linear(x, w, "bf16"), want.to(torch.bfloat16))
+    assert (want != S.exact(x, w)).double().mean() > 0.5
+
+
+def test_groups_are_of_eight_consecutive_elements():
+    # a large pair in every fourth group, alone there: the others' sums are whole
+    T, K, N = 7, 1024, 48
+    x, w = S.tokens(T, K, 3), S.weights(N, K, 4)
+    group, at = torch.arange(K) // 8, torch.arange(K) % 8
+    x[:, (group % 4 != 1) & (at < 2)] = S.ONE
+    w[:, (group % 4 == 1) & (at >= 2)] = 0.0
+    assert torch.equal(_linear(x, w, "bf16"), S.exact(x, w).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 1024, 300), (16, 300, 520), (16, 264, 4104), (40, 700, 200), (150, 256, 264)])
+def test_bfloat16_blocks_lose_what_is_stated(T, H, I):
+    say(f"stated block T={T} H={H} I={I}")
+    x, w = S.tokens(T, H, 1), S.block(H, I, 2, alone=True)
+    cfg = moe.make_mx_ffn_cfg(H, I, "relu", "bf16", "e4m3")
+    y = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device=DEV)
+    moe.mx_ffn_forward(cfg, _upload(x, "e4m3"), {k: _upload(v, "e2m1") for k, v in w.items()}, y,
+                       moe.alloc_mx_ffn_workspace(cfg, T, DEV))
+    for t in range(T):
+        mid, want = S.through(x[t:t + 1], w, S.one_instruction)
+        assert torch.equal(M.rounded(mid, "e4m3"), mid) and (mid > 0).double().mean() > 0.3
+        assert torch.equal(y[t].cpu(), want[0].to(torch.bfloat16)), t

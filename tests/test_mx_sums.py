@@ -33,7 +33,7 @@ def test_the_block_shows_a_product_in_one_instruction(T, H, I):
     assert torch.equal(parts, want)
     up_only = torch.relu(S.one_instruction(x, w["w_gate"])) * S.one_instruction(x, w["w_up"])
     assert (up_only != mid).double().mean() > 0.7            # the up projection's loss alone shows
-    down_only = S.one_instruction(mid * 64, w["w_down"]) / 64
+    down_only = S.one_instruction(mid * 64, w["w_down"], torch.full_like(mid, 1 / 64))
     assert (down_only != want).double().mean() > 0.5         # and the down projection's
 
 
@@ -51,12 +51,9 @@ def test_general_tolerances_do_not_show_it():
         return M.values(c, s, form, cols), torch.exp2(s.to(M.F64) - 127).repeat_interleave(32, 1)[:, :cols]
 
     def product(x, sx, w, sw):
-        # blocks one after the other: elements in one instruction, then their scales
-        y = 0
-        for k in range(0, x.shape[1], 32):
-            at = slice(k, k + 32)
-            y = y + S.one_instruction(x[:, at] / sx[:, at], w[:, at] / sw[:, at]) * sx[:, k:k + 1] * sw[None, :, k]
-        return y
+        # blocks one after the other, with the weights' scales
+        at = [slice(k, k + 32) for k in range(0, x.shape[1], 32)]
+        return sum(S.one_instruction(x[:, b] / sx[:, b], w[:, b] / sw[:, b], sx[:, b]) * sw[None, :, b.start] for b in at)
 
     x = apart(*values(T, H, "e4m3", 1.0)[1], "e4m3", H)
     w = {k: apart(*values(r, c, "e2m1", c ** -0.5)[1], "e2m1", c)
