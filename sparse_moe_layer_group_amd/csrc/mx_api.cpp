@@ -33,7 +33,9 @@ int validate(const moe_mx_ffn_cfg* c, int64_t T) {
   return MOE_OK;
 }
 
-// Room for the parts of split contractions: of T tokens' and every smaller batch's
+// Room for the parts of split contractions: of T tokens' and every smaller batch's.
+// Few tokens have none: nothing but a size that is not 0, which a query has for
+// what is invalid, and a call asks for what its query said.
 struct LinearWork {
   float* part;
   size_t bytes;
