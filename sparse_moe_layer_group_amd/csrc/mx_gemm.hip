@@ -27,18 +27,25 @@
 // used.
 //
 // Outputs are stored past the caches, which then keep the operands for the tiles to
-// come: 4096 x 7168 x 7168 175 -> 162 us, in 4 bits 140 -> 121, 8192 x 7168 x 2048 in 4
-// bits 73 -> 65.  (The residual copied past them too: 132 instead of 124 with 4 bits.)
+// come (us a call without a residual, stored so and not): 8192 x 7168 x 7168 305 and
+// 318, in 4 bits 220 and 251; 8192 x 2048 x 7168 113 and 123, 90 and 104; 2048 x 2048 x
+// 7168 29 and 31; 17 to 1024 tokens within 0.6 either way.  With a norm behind it that
+// reads the output: 8192 x 7168 x 7168 392 and 397, 4 bits 317 and 326, 2048 85 and 88,
+// 17 to 1024 tokens within 0.4.  (The residual copied past them too: 132 instead of 124
+// for 8192 x 2048 x 7168 with 4 bits.)
 //
-// Measured (tokens x in x out, a call): 8192 x 7168 x 7168 with a residual, 8-bit
-// tokens 330 us (2.6 PFLOP/s), 4-bit 258 (3.3); 8192 x 7168 x 2048 85 to 94 and 65; 8192 x
-// 2048 x 7168 127 to 136 and 103 to 116, of which the residual, 117 MB, is 20.  A 256 x
-// 256 tile's step takes 1.32 and 0.92 us; without its copies 1.06 and 0.69, without its
-// LDS reads too 0.97 and 0.62, the instructions' own time at the clock that this load
-// leaves.  Matrix cores busy by counters: gate and up of 8192 tokens 59% of the time,
-// 4096 x 7168 x 7168 51% (448 tiles, 1.75 turns of the chip), 8192 x 7168 x 2048 in 4
-// bits 30%, a single turn of 52 us in the loop and some 12 beside it, and what bias,
-// residual and output take.
+// Measured (tokens x in x out, us a call with a residual, calls running on): 8192 x
+// 7168 x 7168, 8-bit tokens 325 (2.6 PFLOP/s), 4-bit 246 (3.4); 4096 x 7168 x 7168 158 to
+// 165 and 116; 8192 x 7168 x 2048 84 and 63; 8192 x 2048 x 7168 127 and 104, of which
+// the residual, 117 MB, is 20.  The first hundred or so calls after a pause take longer,
+// as kernels as well: 4096 x 7168 x 7168 191, then 177, then 162.  A 256 x 256 tile's step
+// takes 1.32 and 0.92 us; without its copies 1.06 and 0.69, without its LDS reads too 0.97
+// and 0.62, the instructions' own time at the clock that this load leaves.  Matrix cores
+// busy by counters: gate and up of 8192 tokens 59% of the time, 4096 x 7168 x 7168 51%
+// (448 tiles, 1.75 turns of the chip), 8192 x 7168 x 2048 in 4 bits 30%, a single turn of
+// 52 us in the loop and some 12 beside it, and what bias, residual and output take.
+// float32 outputs of 8-bit tokens: 4096 x 7168 x 7168 595, 1024 170, 333 122, 50 33; of
+// 4-bit ones, whose epilogue has neither image nor rows ahead, 162, 47, 23 and 14.
 // Measured and not kept: copies staggered over the waves or issued early in a step
 // (equal or slower), eight stages (no change), waves in two groups that split the
 // contraction (no gain), 32x32x64 instructions (no faster).
@@ -608,6 +615,11 @@ template <int FORM, bool EXACT, int TM, int TN> hipError_t launch_tile(const MxA
 // 168, 145, 136; 8192 x 1024 x 7168 128 x 128 80.7, 256 x 256 89.9.  Of 15 sizes and both
 // forms the rule took the fastest or one within 3% of it, but for 50 x 7168 x 7168 in
 // 4 bits (14.2 by 64 x 64, 13.3 by 64 x 128).
+// `exact` products are planned by the same figures, although a step of theirs is three
+// instructions and the masks: what is taken is right for many tokens (64 x 64, 64 x 128,
+// 128 x 128: 1024 x 7168 x 7168 234, 179, 170; 4096 906, 627, 594; 8192 x 2048 x 7168 560,
+// 401, 384; the last is taken) and not for few (50 x 7168 x 7168 33 taken, 25 by 64 x 128;
+// 333 122 taken, 91 by 64 x 128; 333 x 7168 x 2048 55 taken, 40 by 64 x 128).
 struct TileCost {
   int tm, tn;  // token rows, weight rows
   float step, rest;

@@ -268,8 +268,16 @@ int norm_options(const NormArgs& a) {
 // 32 lanes; of 4-bit codes every other lane stores its own and its neighbour's.
 //
 // From registers, so h is not stored and read again: 8192 rows of 7168 in bfloat16
-// to 8 bits, u beside them, 92 us (413 MB, 4.5 TB/s), where the norm alone takes 96
-// and quantising its output another 34; one row 4.4.
+// to 8 bits, u beside them, 86 to 95 us (413 MB, 4.4 to 4.8 TB/s), where the norm
+// alone takes 96 and quantising its output another 34; one row 4.2.
+// Ragged widths pay for their 32 lanes a block and their byte stores: 8192 rows
+// of 7169 in bfloat16 to 8 bits 190 us (the norm alone 111), as a layer norm 273
+// (174), in float32 191 (190) and 214 (195); of 1001 23 (of 1000: 12), 26 (13), 25
+// (19) and 27 (19).  Past 8192 columns four vectors, their parameters and the blocks'
+// scales do not fit: ragged rows put 64 to 200 registers out to memory in bfloat16 and
+// 215 to 421 in float32, whole ones none and 5 to 140.  2048 rows of 9001: 174 us (81
+// alone), layer norm 352 (109), float32 451 (107) and 544 (278); of 16384: 61 (53), 69
+// (61), 112 (114) and 195 (185).
 template <int FORM, bool WHOLE>
 MOE_DEV void put_mx(uint8_t* codes, uint8_t* scales, const Cols<WHOLE>& c, int j, float (&v)[8]) {
   const int end = (c.H + 127) & ~127;
